@@ -1,0 +1,421 @@
+// Low-rank adapters of many requests beside one projection: the plan that
+// orders a batch's rows by adapter, and
+//   out[r] = base[r] + s_a (x[r] A_a^T) B_a^T,   a = the row's adapter.
+// A_a is [R, d], B_a [N, R] (both K-major like the library's weights).
+//
+// Forward, one launch.  A tile is up to MT rows of one adapter (16, or 64 when
+// adapters have more rows); a cluster of up to eight CTAs shares it.  CTA q
+// multiplies the q-th slice of x's columns with A_a, the cluster's partial
+// x A^T meet through distributed shared memory in rank order, and CTA q then
+// adds its slice of the N output columns.  x, base and out cross HBM once and
+// h = x A^T never leaves the chip (unless the caller wants it kept).
+//
+// The kernel is bound by memory (2 R FLOP per element read at R <= 128), so
+// operands go from global memory straight into mma fragments, 16 bytes a lane:
+// a product does not depend on the order of its inner index, so lane c of a
+// quad takes 8 consecutive inner elements as its share of two k16 steps, and
+// the columns of an output block are dealt to the mma's n index so that a lane
+// holds 8 consecutive ones.  No shared-memory staging, full sectors both ways.
+//
+// h enters the second product as two bf16 terms (hi + lo, 16 bits of mantissa
+// together): one bf16 term alone would put its own rounding, 2^-9 a value,
+// beside that of a bf16 result and dominate an fp32 one.
+#include <cstdint>
+
+#include "common.cuh"
+#include "lora.cuh"
+
+namespace moe {
+namespace {
+
+// ---------------------------------------------------------------- plan
+// Stable counting sort of the rows by adapter; rows without one (-1) last.
+// Two launches: each block counts its rows' adapters; then each block sums the
+// counts before its own (at most kPlanBlocks blocks) and ranks its rows.
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanBlocks = 128;
+
+int plan_rows_per_block(int rows) {
+  const int per = (rows + kPlanBlocks - 1) / kPlanBlocks;
+  return (per + kPlanThreads - 1) / kPlanThreads * kPlanThreads;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_hist_kernel(const int32_t* __restrict__ adapter, int rows, int n,
+                                                                 int per, int32_t* __restrict__ cnt,
+                                                                 int32_t* __restrict__ err) {
+  pdl_wait();
+  pdl_launch_dependents();
+  __shared__ int s_cnt[kMaxAdapters + 1];
+  for (int e = threadIdx.x; e <= n; e += kPlanThreads) s_cnt[e] = 0;
+  __syncthreads();
+  const long long r0 = static_cast<long long>(blockIdx.x) * per;
+  bool bad = false;
+  for (long long r = r0 + threadIdx.x; r < min(r0 + per, static_cast<long long>(rows)); r += kPlanThreads) {
+    const int a = adapter[r];
+    bad |= a < -1 || a >= n;
+    atomicAdd(&s_cnt[a >= 0 && a < n ? a : n], 1);
+  }
+  bad = __syncthreads_or(bad);
+  for (int e = threadIdx.x; e <= n; e += kPlanThreads) cnt[static_cast<size_t>(blockIdx.x) * (n + 1) + e] = s_cnt[e];
+  if (threadIdx.x == 0) err[blockIdx.x] = bad;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_order_kernel(const int32_t* __restrict__ adapter, int rows, int n,
+                                                                  int per, int blocks,
+                                                                  const int32_t* __restrict__ cnt,
+                                                                  const int32_t* __restrict__ err,
+                                                                  int32_t* __restrict__ offsets,
+                                                                  int32_t* __restrict__ order, int* status) {
+  pdl_wait();
+  pdl_launch_dependents();
+  __shared__ int s_at[kMaxAdapters + 1];   // next position of each adapter's rows in this block
+  __shared__ int s_warp[32];
+  __shared__ int s_base;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) s_base = 0;
+  __syncthreads();
+  for (int e0 = 0; e0 <= n; e0 += kPlanThreads) {  // exclusive scan over the adapters, 1024 at a time
+    const int e = e0 + tid;
+    int before = 0, all = 0;
+    if (e <= n) {
+#pragma unroll 8
+      for (int b = 0; b < blocks; ++b) {
+        const int c = cnt[static_cast<size_t>(b) * (n + 1) + e];
+        before += b < static_cast<int>(blockIdx.x) ? c : 0;
+        all += c;
+      }
+    }
+    int incl = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int pre = s_base;
+    for (int w = 0; w < warp; ++w) pre += s_warp[w];
+    const int start = pre + incl - all;
+    if (e <= n) {
+      s_at[e] = start + before;
+      if (blockIdx.x == 0) offsets[e] = start;   // offsets[n]: the rows that have an adapter
+    }
+    __syncthreads();
+    if (tid == kPlanThreads - 1) s_base = start + all;
+    __syncthreads();
+  }
+  const long long r0 = static_cast<long long>(blockIdx.x) * per;
+  for (long long c0 = r0; c0 < min(r0 + per, static_cast<long long>(rows)); c0 += kPlanThreads) {
+    const long long r = c0 + tid;
+    const bool live = r < rows;
+    int a = live ? adapter[r] : -2;
+    if (live && (a < 0 || a >= n)) a = n;
+    const unsigned same = __match_any_sync(0xffffffffu, a);
+    const int rank = __popc(same & ((1u << lane) - 1));
+    int at = 0;
+    for (int w = 0; w < 32; ++w) {  // warps in row order
+      if (warp == w && live) at = s_at[a];
+      __syncthreads();
+      if (warp == w && live && rank == 0) s_at[a] = at + __popc(same);
+      __syncthreads();
+    }
+    if (live) order[at + rank] = static_cast<int32_t>(r);
+  }
+  if (blockIdx.x == 0) {
+    bool bad = false;
+    for (int b = tid; b < blocks; b += kPlanThreads) bad |= err[b] != 0;
+    bad = __syncthreads_or(bad);
+    if (tid == 0) *status = bad ? MOE_ERR_INVALID : MOE_OK;
+  }
+}
+
+__global__ void plan_empty_kernel(int n, int32_t* offsets, int* status) {
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int e = threadIdx.x; e <= n; e += blockDim.x) offsets[e] = 0;
+  if (threadIdx.x == 0) *status = MOE_OK;
+}
+
+// ---------------------------------------------------------------- forward
+constexpr int kLoraThreads = 256;
+
+struct LoraArgs {
+  const __nv_bfloat16* x;
+  const __nv_bfloat16* A;
+  const __nv_bfloat16* B;
+  const float* scale;
+  const int32_t* offsets;
+  const int32_t* order;
+  int n, rows, d, N, R;
+  const void* base;
+  void* out;
+  float* h_out;
+  int kslice, nslice;   // columns of x / of out a CTA of the cluster takes, multiples of 32
+};
+
+template <int RP, int MT>
+struct LoraTile {
+  static constexpr int MW = RP <= 64 && MT >= 32 ? 2 : 1;   // m16 tiles a warp holds
+  static constexpr int WM = MT / (16 * MW);                 // warps along the rows
+  static constexpr int WK = 8 / WM;                         // warps along the columns
+  static constexpr int HS = RP + 8;                         // row stride of the bf16 h terms: spreads the banks
+  static constexpr int RED = WK * MT * RP * 4;              // the warps' partial sums; then h's two terms
+  static constexpr int HB = 2 * MT * HS * 2;
+  static constexpr int SMEM = (RED > HB ? RED : HB) + MT * RP * 4;
+  static constexpr int UK = RP <= 16 ? 4 : RP <= 64 ? 2 : 1;  // k32 steps loaded ahead
+};
+
+template <int RP, int MT, typename OT>
+__global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraArgs p) {
+  using L = LoraTile<RP, MT>;
+  constexpr int MW = L::MW, WM = L::WM, WK = L::WK, HS = L::HS;
+  pdl_wait();
+  pdl_launch_dependents();
+  extern __shared__ __align__(16) uint8_t s_raw[];
+  float* s_red = reinterpret_cast<float*>(s_raw);                        // [WK][MT][RP]
+  __nv_bfloat16* s_hi = reinterpret_cast<__nv_bfloat16*>(s_raw);         // [MT][HS], after the sums are read
+  __nv_bfloat16* s_lo = s_hi + MT * HS;
+  float* s_part = reinterpret_cast<float*>(s_raw + L::SMEM - MT * RP * 4);  // [MT][RP]: this CTA's slice of h
+  __shared__ int s_row[MT];
+
+  const uint32_t CS = cluster_size(), rank = cluster_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, c = lane & 3;
+  int a, start, end;
+  if (!find_tile<MT>(p.offsets, p.n, p.rows, blockIdx.x / CS, a, start, end)) return;  // the whole cluster leaves
+  if (tid < MT) {
+    int r = start + tid < end ? p.order[start + tid] : -1;
+    s_row[tid] = r >= 0 && r < p.rows ? r : -1;
+  }
+  __syncthreads();
+
+  const int n0 = rank * p.nslice, n1 = min(p.N, n0 + p.nslice);
+  OT* out = static_cast<OT*>(p.out);
+  const OT* base = static_cast<const OT*>(p.base);
+  if (a == p.n) {  // rows without an adapter
+    if (p.h_out)
+      for (int i = tid; i < MT * p.R; i += kLoraThreads)
+        if (i / p.R % CS == rank && s_row[i / p.R] >= 0) p.h_out[static_cast<size_t>(s_row[i / p.R]) * p.R + i % p.R] = 0.f;
+    if (base == out) return;
+    const int w8 = (n1 - n0) / 8;
+    for (int i = tid; i < MT * w8; i += kLoraThreads) {
+      const int r = s_row[i / w8];
+      if (r < 0) continue;
+      const size_t o = static_cast<size_t>(r) * p.N + n0 + i % w8 * 8;
+      float v[8] = {};
+      if (base) load8(base + o, v);
+      store8(out + o, v);
+    }
+    return;
+  }
+
+  // ---- h over this CTA's columns of x
+  const int wm = warp % WM, wk = warp / WM;
+  {
+    float acc[MW][RP / 8][4];
+#pragma unroll
+    for (int m = 0; m < MW; ++m)
+#pragma unroll
+      for (int j = 0; j < RP / 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.f;
+    const __nv_bfloat16* xr[MW][2];
+    bool xl[MW][2];
+#pragma unroll
+    for (int m = 0; m < MW; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = s_row[(wm * MW + m) * 16 + g + 8 * h];
+        xl[m][h] = r >= 0;
+        xr[m][h] = p.x + static_cast<size_t>(r >= 0 ? r : 0) * p.d + c * 8;
+      }
+    const __nv_bfloat16* Ar = p.A + (static_cast<size_t>(a) * p.R + g) * p.d + c * 8;
+    const int k0 = rank * p.kslice, k1 = min(p.d, k0 + p.kslice);
+    for (int kb = k0 + wk * 32; kb < k1; kb += WK * 32 * L::UK) {
+      uint4 xv[L::UK][MW][2], av[L::UK][RP / 8];
+#pragma unroll
+      for (int u = 0; u < L::UK; ++u) {
+        const int k = kb + u * WK * 32;
+        const bool in = k + c * 8 < k1;
+#pragma unroll
+        for (int m = 0; m < MW; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) xv[u][m][h] = in && xl[m][h] ? ldg_stream(xr[m][h] + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < RP / 8; ++j)
+          av[u][j] = in && j * 8 + g < p.R ? ldg16(Ar + static_cast<size_t>(j * 8) * p.d + k) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int u = 0; u < L::UK; ++u)
+#pragma unroll
+        for (int m = 0; m < MW; ++m)
+#pragma unroll
+          for (int j = 0; j < RP / 8; ++j) {
+            mma16816(acc[m][j], xv[u][m][0].x, xv[u][m][1].x, xv[u][m][0].y, xv[u][m][1].y, av[u][j].x, av[u][j].y);
+            mma16816(acc[m][j], xv[u][m][0].z, xv[u][m][1].z, xv[u][m][0].w, xv[u][m][1].w, av[u][j].z, av[u][j].w);
+          }
+    }
+#pragma unroll
+    for (int m = 0; m < MW; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float* o = s_red + (static_cast<size_t>(wk) * MT + (wm * MW + m) * 16 + g + 8 * h) * RP + 2 * c;
+#pragma unroll
+        for (int j = 0; j < RP / 8; ++j)
+          *reinterpret_cast<float2*>(o + 8 * j) = make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
+      }
+  }
+  __syncthreads();
+  for (int i = tid; i < MT * RP / 4; i += kLoraThreads) {
+    float4 v = reinterpret_cast<const float4*>(s_red)[i];
+#pragma unroll
+    for (int w = 1; w < WK; ++w) {
+      const float4 u = reinterpret_cast<const float4*>(s_red + w * MT * RP)[i];
+      v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+    }
+    reinterpret_cast<float4*>(s_part)[i] = v;
+  }
+  cluster_arrive();
+  cluster_wait();   // every CTA's slice is there (CS = 1: the block's own barrier)
+  const float sc = p.scale ? __ldg(p.scale + a) : 1.f;
+  for (int i = tid; i < MT * RP / 4; i += kLoraThreads) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (uint32_t q = 0; q < CS; ++q) {
+      const float4 u = ld_cluster(reinterpret_cast<const float4*>(s_part) + i, q);
+      v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+    }
+    const int m = i / (RP / 4), j = i % (RP / 4) * 4;
+    if (p.h_out && m % CS == rank && s_row[m] >= 0 && j < p.R)
+      *reinterpret_cast<float4*>(p.h_out + static_cast<size_t>(s_row[m]) * p.R + j) = v;
+    split_store(s_hi + m * HS + j, s_lo + m * HS + j, v, sc);
+  }
+  cluster_arrive();  // done with the others' shared memory; waited for before this CTA ends
+  __syncthreads();
+
+  // ---- out over this CTA's columns
+  uint32_t hh[MW][RP / 16][4], hl[MW][RP / 16][4];
+#pragma unroll
+  for (int m = 0; m < MW; ++m) {
+    const int r = (wm * MW + m) * 16 + g;
+    load_terms<RP>(s_hi + r * HS, s_hi + (r + 8) * HS, c, hh[m]);
+    load_terms<RP>(s_lo + r * HS, s_lo + (r + 8) * HS, c, hl[m]);
+  }
+  size_t ro[MW][2];
+  bool rl[MW][2];
+#pragma unroll
+  for (int m = 0; m < MW; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = s_row[(wm * MW + m) * 16 + g + 8 * h];
+      rl[m][h] = r >= 0;
+      ro[m][h] = static_cast<size_t>(r >= 0 ? r : 0) * p.N + c * 8;
+    }
+  // the mma's n index g of block t is column (g / 2) * 8 + 2 t + g % 2 of 32
+  const __nv_bfloat16* Bc = p.B + (static_cast<size_t>(a) * p.N + (g >> 1) * 8 + (g & 1)) * p.R;
+  for (int nb = n0 + wk * 32; nb < n1; nb += WK * 32) {
+    float acc[MW][4][4];
+    const bool in = nb + c * 8 < n1;
+#pragma unroll
+    for (int m = 0; m < MW; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float v[8] = {};
+        if (base && in && rl[m][h]) load8(base + ro[m][h] + nb, v);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[m][t][2 * h] = v[2 * t], acc[m][t][2 * h + 1] = v[2 * t + 1];
+      }
+    const bool bin = nb + (g >> 1) * 8 < n1;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      uint32_t b[RP / 16][2];
+      load_b_row<RP>(Bc + static_cast<size_t>(nb + 2 * t) * p.R, bin, p.R, c, b);
+#pragma unroll
+      for (int k = 0; k < RP / 16; ++k)
+#pragma unroll
+        for (int m = 0; m < MW; ++m) {
+          mma16816(acc[m][t], hl[m][k][0], hl[m][k][1], hl[m][k][2], hl[m][k][3], b[k][0], b[k][1]);
+          mma16816(acc[m][t], hh[m][k][0], hh[m][k][1], hh[m][k][2], hh[m][k][3], b[k][0], b[k][1]);
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < MW; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (!in || !rl[m][h]) continue;
+        float v[8];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) v[2 * t] = acc[m][t][2 * h], v[2 * t + 1] = acc[m][t][2 * h + 1];
+        store8(out + ro[m][h] + nb, v);
+      }
+  }
+  cluster_wait();
+}
+
+template <int RP, int MT, typename OT>
+int launch_lora_tile(const LoraArgs& p, int cs, cudaStream_t s) {
+  using L = LoraTile<RP, MT>;
+  auto kernel = lora_kernel<RP, MT, OT>;
+  static std::atomic<uint64_t> done{0};
+  const int st = allow_smem(done, kernel, L::SMEM);
+  if (st != MOE_OK) return st;
+  const long long tiles = tile_slots<MT>(p.rows, p.n);
+  return launch_cluster("lora_kernel", kernel, dim3(static_cast<unsigned>(tiles * cs)), dim3(kLoraThreads), L::SMEM, cs, s, p);
+}
+
+template <int RP, typename OT>
+int launch_lora_rows(LoraArgs& p, cudaStream_t s) {
+  const bool wide = p.rows > 16ll * p.n;  // more than one 16-row tile to an adapter
+  const int mt = wide ? 64 : 16;
+  // CTAs to fill the SMs twice, each with at least 128 columns of the wider side
+  const long long tiles = static_cast<long long>(p.rows) / mt + p.n;
+  const int widest = p.d > p.N ? p.d : p.N;
+  int cs = 1;
+  while (cs < 8 && tiles * cs < 4ll * num_sms() && widest >= cs * 2 * 128) cs *= 2;
+  p.kslice = ((p.d + cs - 1) / cs + 31) / 32 * 32;
+  p.nslice = ((p.N + cs - 1) / cs + 31) / 32 * 32;
+  return wide ? launch_lora_tile<RP, 64, OT>(p, cs, s) : launch_lora_tile<RP, 16, OT>(p, cs, s);
+}
+
+template <typename OT>
+int launch_lora_rank(LoraArgs& p, cudaStream_t s) {
+  if (p.R <= 16) return launch_lora_rows<16, OT>(p, s);
+  if (p.R <= 32) return launch_lora_rows<32, OT>(p, s);
+  if (p.R <= 64) return launch_lora_rows<64, OT>(p, s);
+  return launch_lora_rows<128, OT>(p, s);
+}
+
+}  // namespace
+
+size_t adapter_plan_workspace_bytes(int rows, int n) {
+  const int per = plan_rows_per_block(rows);
+  const size_t blocks = rows > 0 ? (rows + static_cast<size_t>(per) - 1) / per : 0;
+  return 256 + align_up(blocks * (n + 1) * 4, 256) + align_up(blocks * 4, 256);
+}
+
+int launch_adapter_plan(const int32_t* adapter, int rows, int n, int32_t* offsets, int32_t* order, void* ws,
+                        cudaStream_t s) {
+  int* status = static_cast<int*>(ws);
+  if (rows == 0) return launch_pdl(__func__, plan_empty_kernel, dim3(1), dim3(256), 0, s, n, offsets, status);
+  const int per = plan_rows_per_block(rows);
+  const int blocks = static_cast<int>((static_cast<long long>(rows) + per - 1) / per);
+  int32_t* cnt = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + 256);
+  int32_t* err = cnt + align_up(static_cast<size_t>(blocks) * (n + 1) * 4, 256) / 4;
+  const int st = launch_pdl(__func__, plan_hist_kernel, dim3(blocks), dim3(kPlanThreads), 0, s, adapter, rows, n, per,
+                            cnt, err);
+  if (st != MOE_OK) return st;
+  return launch_pdl(__func__, plan_order_kernel, dim3(blocks), dim3(kPlanThreads), 0, s, adapter, rows, n, per, blocks,
+                    static_cast<const int32_t*>(cnt), static_cast<const int32_t*>(err), offsets, order, status);
+}
+
+int launch_lora(const void* x, const void* A, const void* B, const float* scale, const int32_t* offsets,
+                const int32_t* order, int n, int rows, int d, int N, int R, const void* base, void* out, int out_dtype,
+                float* h_out, cudaStream_t s) {
+  if (rows == 0) return MOE_OK;
+  LoraArgs p{};
+  p.x = static_cast<const __nv_bfloat16*>(x), p.A = static_cast<const __nv_bfloat16*>(A);
+  p.B = static_cast<const __nv_bfloat16*>(B), p.scale = scale, p.offsets = offsets, p.order = order;
+  p.n = n, p.rows = rows, p.d = d, p.N = N, p.R = R, p.base = base, p.out = out, p.h_out = h_out;
+  return out_dtype == MOE_F32 ? launch_lora_rank<float>(p, s) : launch_lora_rank<__nv_bfloat16>(p, s);
+}
+
+}  // namespace moe

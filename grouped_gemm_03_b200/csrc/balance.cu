@@ -1,0 +1,571 @@
+// Training the router: the balance loss over sequences with its per-expert
+// counts, and the gradient of the router's logits (gates and balance loss in
+// one pass over them).
+//
+// Loss ("MegaMoE ..." §2: alpha * E * sum_i f_i P_i, here per sequence): with
+// p = softmax(logits), c[s,e] the (token, slot) pairs of sequence s that chose
+// expert e, Q[s,e] the sum of p over its N_s tokens, and S' the sequences that
+// have tokens,
+//   loss = sum_s coef_s sum_e c[s,e] Q[s,e],   coef_s = alpha E / (k N_s^2 S'),
+// which is the mean over sequences of alpha E sum_e f_e P_e with
+// f = c / (k N) and P = Q / N.
+//
+// Gradient: both the raw gates (w_j = p at topk_idx_j) and the loss are linear
+// in p, so with G_e = sum_{j: idx_j = e} dw_j + dloss coef_s c[s,e]
+//   dlogit_e = p_e (G_e - sum_i G_i p_i).
+// Renormalised gates are a softmax over the selected experts alone:
+//   w_j = p_j / sum_S p,   dlogit_{idx_j} += w_j (dw_j - sum_S w dw).
+//
+// Both kernels are bound by reading the logits (and writing their gradient):
+// one pass, each row held in registers by L lanes (4 columns a lane up to 128
+// experts, then 8, 16, 32), the softmax's maximum and sum by shuffles.
+#include "common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kBalThreads = 256;
+constexpr int kBalMinChunk = 32;     // tokens of one block, at least
+constexpr int kBalMaxChunks = 592;   // blocks of the first pass: four on each of 148 SMs
+constexpr int kFinThreads = 1024;
+constexpr int kFinCluster = 8;       // CTAs of the second pass, each a slice of the experts
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __half* p) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                     __uint_as_float(v.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__half* p, float4 v) {
+  const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+__device__ __forceinline__ float from_f32(float v, float) { return v; }
+__device__ __forceinline__ __half from_f32(float v, __half) { return __float2half_rn(v); }
+__device__ __forceinline__ __nv_bfloat16 from_f32(float v, __nv_bfloat16) { return __float2bfloat16_rn(v); }
+
+// Lane l of the L lanes of a row holds columns (i * L + l) * 4 + c, c < 4, as v[4 * i + c].
+template <typename T, int V>
+__device__ __forceinline__ void load_row(const T* row, int E, int L, int l, bool vec, bool live, float (&v)[V]) {
+#pragma unroll
+  for (int i = 0; i < V / 4; ++i) {
+    const int c = (i * L + l) * 4;
+    float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    if (live) {
+      if (vec) {
+        if (c < E) f = load4(row + c);
+      } else {
+        if (c < E) f.x = to_f32(row[c]);
+        if (c + 1 < E) f.y = to_f32(row[c + 1]);
+        if (c + 2 < E) f.z = to_f32(row[c + 2]);
+        if (c + 3 < E) f.w = to_f32(row[c + 3]);
+      }
+    }
+    v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
+  }
+}
+
+__device__ __forceinline__ float group_max(float v, int L) {
+  for (int o = L >> 1; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float group_sum(float v, int L) {
+  for (int o = L >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Softmax of a row in place.  A logit of -inf has probability 0; a row of
+// nothing else (a row that is not live is one) has probability 0 throughout.
+// The maximum passes over a NaN, the sum does not, so a NaN logit makes its
+// row NaN.
+template <int V>
+__device__ __forceinline__ void softmax_row(float (&v)[V], int L) {
+  float m = v[0];
+#pragma unroll
+  for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
+  m = group_max(m, L);
+  if (m == -INFINITY) m = 0.f;
+  float z = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    v[i] = __expf(v[i] - m);
+    z += v[i];
+  }
+  z = group_sum(z, L);
+  const float inv = z == 0.f ? 0.f : __fdividef(1.f, z);
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] *= inv;
+}
+
+// First token at or after `t` belongs to the sequence this returns: the number
+// of sequences that end at or before t (all threads of the block take part).
+__device__ int sequence_at(const int32_t* off, int S, int t) {
+  int n = 0;
+  for (int s0 = 0; s0 < S; s0 += blockDim.x) {
+    const int s = s0 + threadIdx.x;
+    n += __syncthreads_count(s < S && off[s + 1] <= t);
+  }
+  return n;
+}
+
+struct BalanceArgs {
+  const void* logits;
+  const int32_t* idx;
+  int T, E, k;
+  const int32_t* off;   // [S + 1] or nullptr: one sequence of all T tokens
+  int S;
+  const uint8_t* mask;  // [T] or nullptr
+  float alpha;
+  int chunk, chunks, L, vec;
+  // partial sums by slot = chunk index + sequence index: along the tokens at
+  // least one of the two grows from a segment to the next, so slots differ
+  float* part_q;        // [chunks + S][E]
+  int32_t* part_c;      // [chunks + S][E]
+  int32_t* part_n;      // [chunks + S]
+  int32_t* part_err;    // [chunks]
+  float* loss;
+  int32_t* counts;
+  float* prob;
+  float* coef;
+  int* status;
+};
+
+// First pass: block b sums the probabilities and counts of its chunk of
+// tokens, for each sequence in it.
+template <typename T, int V>
+__global__ void __launch_bounds__(kBalThreads) balance_partial_kernel(const BalanceArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  extern __shared__ float s_mem[];
+  const int E = a.E, L = a.L;
+  const int width = L * V;                                    // padded columns
+  float* s_q = s_mem;                                          // [8 warps][width]
+  int* s_c = reinterpret_cast<int*>(s_mem + (kBalThreads / 32) * width);  // [E]
+  __shared__ int s_err;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int l = lane % L, group = tid / L, groups = kBalThreads / L;
+  const T* logits = static_cast<const T*>(a.logits);
+  const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
+  if (tid == 0) s_err = 0;
+  for (int e = tid; e < E; e += kBalThreads) s_c[e] = 0;
+  int s = 0;
+  if (a.off) {
+    // each block checks its share of the offsets
+    const int per = (a.S + a.chunks - 1) / a.chunks;
+    bool bad = blockIdx.x == 0 && tid == 0 && a.off[0] != 0;
+    for (int i = blockIdx.x * per + tid; i < min(a.S, (static_cast<int>(blockIdx.x) + 1) * per); i += kBalThreads)
+      bad |= a.off[i] > a.off[i + 1] || a.off[i + 1] > a.T;
+    s = sequence_at(a.off, a.S, t0);
+    if (bad) atomicOr(&s_err, 2);
+  }
+  __syncthreads();
+  int t = t0;
+  while (t < t1 && s < a.S) {
+    const int end = a.off ? min(t1, a.off[s + 1]) : t1;
+    if (end <= t) {
+      ++s;
+      continue;
+    }
+    const size_t slot = blockIdx.x + static_cast<size_t>(s);
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    // a warp's lanes run the same number of rounds: rows past the end are not live
+    constexpr int U = V <= 4 ? 4 : V <= 8 ? 2 : 1;  // rows loaded ahead of their use
+    for (int b = t; b < end; b += groups * U) {
+      float v[U][V];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = b + u * groups + group;
+        const bool live = r < end && (!a.mask || a.mask[r]);
+        load_row<T, V>(logits + static_cast<size_t>(live ? r : t) * E, E, L, l, a.vec, live, v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        softmax_row<V>(v[u], L);
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] += v[u][i];
+      }
+    }
+    int n = 0;
+    for (int r = t + tid; r < end; r += kBalThreads) n += !a.mask || a.mask[r];
+    const long long p1 = static_cast<long long>(end) * a.k;
+    for (long long p = static_cast<long long>(t) * a.k + tid; p < p1; p += kBalThreads) {
+      if (a.mask && !a.mask[p / a.k]) continue;
+      const int e = a.idx[p];
+      if (e >= 0 && e < E)
+        atomicAdd(&s_c[e], 1);   // whole numbers: the order does not show
+      else if (e != -1)
+        atomicOr(&s_err, 1);
+    }
+    // the warp's rows, then the block's warps, in a fixed order
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      for (int o = L; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+    if (lane < L) {
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i)
+        *reinterpret_cast<float4*>(s_q + warp * width + (i * L + l) * 4) =
+            make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+    }
+    __shared__ int s_n[kBalThreads / 32];
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) s_n[warp] = n;
+    __syncthreads();
+    for (int e = tid; e < E; e += kBalThreads) {
+      float q = 0.f;
+#pragma unroll
+      for (int w = 0; w < kBalThreads / 32; ++w) q += s_q[w * width + e];
+      a.part_q[slot * E + e] = q;
+      a.part_c[slot * E + e] = s_c[e];
+      s_c[e] = 0;
+    }
+    if (tid == 0) {
+      int all = 0;
+      for (int w = 0; w < kBalThreads / 32; ++w) all += s_n[w];
+      a.part_n[slot] = all;
+    }
+    __syncthreads();
+    t = end;
+  }
+  if (tid == 0) a.part_err[blockIdx.x] = s_err;
+}
+
+// Second pass, one cluster: CTA r reduces its slice of the experts over the
+// slots of every sequence, `w` threads to a column and `g` sequences at once;
+// the CTAs' shares of the loss meet in rank order.
+__global__ void __launch_bounds__(kFinThreads) __cluster_dims__(kFinCluster, 1, 1)
+    balance_finish_kernel(const BalanceArgs a, int cols, int w) {
+  pdl_wait();
+  pdl_launch_dependents();
+  __shared__ float s_q[kFinThreads];
+  __shared__ int s_c[kFinThreads];
+  __shared__ int s_tok[kFinThreads];
+  __shared__ float s_loss[kFinCluster];
+  __shared__ int s_live;
+  const int tid = threadIdx.x;
+  uint32_t rank;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  // every CTA of the cluster runs before another one writes to its shared memory (waited for below)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const int E = a.E;
+  auto slots = [&](int s, int& first, int& last) {  // [first, last) of sequence s
+    const int b = a.off ? max(0, min(a.T, a.off[s])) : 0, e = a.off ? max(0, min(a.T, a.off[s + 1])) : a.T;
+    first = e > b ? b / a.chunk + s : 0;
+    last = e > b ? (e - 1) / a.chunk + s + 1 : 0;
+  };
+  // sequences that have tokens
+  int live = 0;
+  for (int s0 = 0; s0 < a.S; s0 += kFinThreads) {
+    bool some = false;
+    if (s0 + tid < a.S) {
+      int f, e;
+      slots(s0 + tid, f, e);
+      for (; f < e && !some; ++f) some = a.part_n[f] > 0;
+    }
+    live += __syncthreads_count(some);
+  }
+  if (tid == 0) s_live = live;
+  const int g = kFinThreads / (cols * w);                   // sequences at once
+  const int col = tid % cols, j = tid / cols % w, sg = tid / (cols * w);
+  const int e = rank * cols + col;
+  float share = 0.f;
+  for (int s0 = 0; s0 < a.S; s0 += g) {
+    const int s = s0 + sg;
+    float q = 0.f;
+    int c = 0, n = 0;
+    if (s < a.S && e < E) {
+      int f, l;
+      slots(s, f, l);
+#pragma unroll 4
+      for (int i = f + j; i < l; i += w) {
+        q += a.part_q[static_cast<size_t>(i) * E + e];
+        c += a.part_c[static_cast<size_t>(i) * E + e];
+        n += a.part_n[i];
+      }
+    }
+    s_q[tid] = q, s_c[tid] = c, s_tok[tid] = n;
+    for (int o = w >> 1; o; o >>= 1) {
+      __syncthreads();
+      if (j < o) {
+        s_q[tid] += s_q[tid + o * cols];
+        s_c[tid] += s_c[tid + o * cols];
+        s_tok[tid] += s_tok[tid + o * cols];
+      }
+    }
+    __syncthreads();
+    if (j == 0 && s < a.S && e < E) {
+      q = s_q[tid], c = s_c[tid], n = s_tok[tid];
+      const float nf = static_cast<float>(n);
+      const float k_s = n > 0 ? __fdiv_rn(a.alpha * E, a.k * nf * nf * static_cast<float>(s_live)) : 0.f;
+      a.counts[static_cast<size_t>(s) * E + e] = c;
+      if (a.prob) a.prob[static_cast<size_t>(s) * E + e] = n > 0 ? __fdiv_rn(q, nf) : 0.f;
+      if (e == 0) a.coef[s] = k_s;
+      share += k_s * (static_cast<float>(c) * q);
+    }
+    __syncthreads();
+  }
+  // the block's share, summed in thread order by halves
+  s_q[tid] = share;
+  for (int o = kFinThreads >> 1; o; o >>= 1) {
+    __syncthreads();
+    if (tid < o) s_q[tid] += s_q[tid + o];
+  }
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  if (tid == 0) {
+    uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(&s_loss[rank])), there;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(there) : "r"(at));
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(s_q[0]) : "memory");
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (rank == 0) {
+    int err = 0;
+    for (int i = tid; i < a.chunks; i += kFinThreads) err |= a.part_err[i];
+    const int bad = __syncthreads_or(err & 2), odd = __syncthreads_or(err & 1);
+    if (tid == 0) {
+      float all = 0.f;
+      for (int r = 0; r < kFinCluster; ++r) all += s_loss[r];
+      *a.loss = all;
+      *a.status = bad ? MOE_ERR_BAD_OFFSETS : odd ? MOE_ERR_INVALID : MOE_OK;
+    }
+  }
+}
+
+struct RouterGradArgs {
+  const void* logits;
+  const int32_t* idx;
+  const float* d_w;      // [T, k] or nullptr
+  int T, E, k, renorm;
+  const int32_t* off;
+  int S;
+  const uint8_t* mask;
+  const int32_t* counts;  // [S, E] or nullptr: no balance loss
+  const float* coef;      // [S]
+  const float* d_loss;    // device scalar or nullptr (1)
+  void* out;
+  int chunk, L, vec;
+};
+
+template <typename T, typename OT, int V>
+__global__ void __launch_bounds__(kBalThreads) router_backward_kernel(const RouterGradArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int E = a.E, L = a.L;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int l = lane % L, group = tid / L, groups = kBalThreads / L;
+  const T* logits = static_cast<const T*>(a.logits);
+  OT* out = static_cast<OT*>(a.out);
+  const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
+  int s = a.counts && a.off ? sequence_at(a.off, a.S, t0) : 0;
+  int held = -1;        // the sequence whose counts are in bal
+  float bal[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) bal[i] = 0.f;
+  const float d_loss = a.counts && a.d_loss ? __ldg(a.d_loss) : 1.f;
+  for (int b = t0; b < t1; b += groups) {
+    const int t = b + group;
+    const bool live = t < t1;
+    const int tr = live ? t : t0;
+    float p[V], G[V];
+    load_row<T, V>(logits + static_cast<size_t>(tr) * E, E, L, l, a.vec, live, p);
+    bool any = false;   // something to differentiate: else the row's gradient is 0 whatever its logits hold
+#pragma unroll
+    for (int i = 0; i < V; ++i) G[i] = 0.f;
+    if (a.counts) {
+      while (a.off && s < a.S && a.off[s + 1] <= tr) ++s;
+      const bool in = s < a.S && (!a.mask || a.mask[tr]);
+      if (in && held != s) {
+        held = s;
+        const float c = __ldg(a.coef + s) * d_loss;
+        const int32_t* n = a.counts + static_cast<size_t>(s) * E;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int e = ((i >> 2) * L + l) * 4 + (i & 3);
+          bal[i] = e < E ? c * static_cast<float>(__ldg(n + e)) : 0.f;
+        }
+      }
+      any = in;
+      if (in) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) G[i] = bal[i];
+      }
+    }
+    const int32_t* idx = a.idx + static_cast<size_t>(tr) * a.k;
+    const float* d_w = a.d_w ? a.d_w + static_cast<size_t>(tr) * a.k : nullptr;
+    if (d_w && !a.renorm) {
+      for (int j = 0; j < a.k; ++j) {
+        const int e = __ldg(idx + j);
+        const float g = __ldg(d_w + j);
+        any |= g != 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) G[i] += ((i >> 2) * L + l) * 4 + (i & 3) == e ? g : 0.f;
+      }
+    }
+    softmax_row<V>(p, L);
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) dot = fmaf(p[i], G[i], dot);
+    dot = group_sum(dot, L);
+#pragma unroll
+    for (int i = 0; i < V; ++i) G[i] = p[i] * (G[i] - dot);
+    if (d_w && a.renorm) {  // over the selected experts: w = p / sum, one expert's weight is exactly 1
+      float z = 0.f;
+      for (int j = 0; j < a.k; ++j) {
+        const int e = __ldg(idx + j);
+        any |= __ldg(d_w + j) != 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) z += ((i >> 2) * L + l) * 4 + (i & 3) == e ? p[i] : 0.f;
+      }
+      z = group_sum(z, L);
+      const float zs = z == 0.f ? 1.f : z;
+      float wd = 0.f;
+      for (int j = 0; j < a.k; ++j) {
+        const int e = __ldg(idx + j);
+        const float g = __ldg(d_w + j);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          wd += ((i >> 2) * L + l) * 4 + (i & 3) == e ? __fdiv_rn(p[i], zs) * g : 0.f;
+      }
+      wd = group_sum(wd, L);
+      for (int j = 0; j < a.k; ++j) {
+        const int e = __ldg(idx + j);
+        const float g = __ldg(d_w + j);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (((i >> 2) * L + l) * 4 + (i & 3) == e) G[i] += __fdiv_rn(p[i], zs) * (g - wd);
+      }
+    }
+    if (!live) continue;
+    OT* row = out + static_cast<size_t>(t) * E;
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+      const int c = (i * L + l) * 4;
+      if (!any) G[4 * i] = G[4 * i + 1] = G[4 * i + 2] = G[4 * i + 3] = 0.f;
+      if (a.vec) {
+        if (c < E) store4(row + c, make_float4(G[4 * i], G[4 * i + 1], G[4 * i + 2], G[4 * i + 3]));
+      } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (c + u < E) row[c + u] = from_f32(G[4 * i + u], OT());
+      }
+    }
+  }
+}
+
+int lanes_for(int E, int V) {  // lanes of a row: a power of two, V columns each
+  int L = 1;
+  while (L < 32 && L * V < E) L *= 2;
+  return L;
+}
+int values_for(int E) { return E <= 128 ? 4 : E <= 256 ? 8 : E <= 512 ? 16 : 32; }
+
+int balance_chunk(int T) {
+  const int c = (T + kBalMaxChunks - 1) / kBalMaxChunks;
+  return c < kBalMinChunk ? kBalMinChunk : c;
+}
+
+template <typename T>
+int launch_partial(const BalanceArgs& a, int V, cudaStream_t s) {
+  const size_t smem = (static_cast<size_t>(kBalThreads / 32) * a.L * V + a.E) * 4;
+  const dim3 grid(a.chunks), block(kBalThreads);
+  switch (V) {
+    case 4: return launch_pdl(__func__, balance_partial_kernel<T, 4>, grid, block, smem, s, a);
+    case 8: return launch_pdl(__func__, balance_partial_kernel<T, 8>, grid, block, smem, s, a);
+    case 16: return launch_pdl(__func__, balance_partial_kernel<T, 16>, grid, block, smem, s, a);
+    default: return launch_pdl(__func__, balance_partial_kernel<T, 32>, grid, block, smem, s, a);
+  }
+}
+
+template <typename T, typename OT>
+int launch_grad(const RouterGradArgs& a, int V, int grid, cudaStream_t s) {
+  const dim3 g(grid), b(kBalThreads);
+  switch (V) {
+    case 4: return launch_pdl(__func__, router_backward_kernel<T, OT, 4>, g, b, 0, s, a);
+    case 8: return launch_pdl(__func__, router_backward_kernel<T, OT, 8>, g, b, 0, s, a);
+    case 16: return launch_pdl(__func__, router_backward_kernel<T, OT, 16>, g, b, 0, s, a);
+    default: return launch_pdl(__func__, router_backward_kernel<T, OT, 32>, g, b, 0, s, a);
+  }
+}
+
+template <typename T>
+int launch_grad_to(const RouterGradArgs& a, int out_dtype, int V, int grid, cudaStream_t s) {
+  if (out_dtype == MOE_F32) return launch_grad<T, float>(a, V, grid, s);
+  if (out_dtype == MOE_F16) return launch_grad<T, __half>(a, V, grid, s);
+  return launch_grad<T, __nv_bfloat16>(a, V, grid, s);
+}
+
+}  // namespace
+
+size_t balance_workspace_bytes(int T, int E, int S) {
+  const size_t chunks = T > 0 ? (T + balance_chunk(T) - 1) / balance_chunk(T) : 0;
+  const size_t slots = chunks + S;
+  return 256 + align_up(slots * E * 4, 256) * 2 + align_up(slots * 4, 256) + align_up(chunks * 4 + 4, 256);
+}
+
+int launch_balance_loss(const void* logits, int dtype, const int32_t* idx, int T, int E, int k, const int32_t* off,
+                        int S, const uint8_t* mask, float alpha, float* loss, int32_t* counts, float* prob,
+                        float* coef, void* ws, cudaStream_t s) {
+  BalanceArgs a{};
+  const int V = values_for(E);
+  a.logits = logits, a.idx = idx, a.T = T, a.E = E, a.k = k, a.off = off, a.S = S, a.mask = mask, a.alpha = alpha;
+  a.chunk = balance_chunk(T);
+  a.chunks = T > 0 ? (T + a.chunk - 1) / a.chunk : 0;
+  a.L = lanes_for(E, V);
+  a.vec = E % 4 == 0;
+  const size_t slots = static_cast<size_t>(a.chunks) + S, m = align_up(slots * E * 4, 256);
+  char* p = static_cast<char*>(ws);
+  a.status = reinterpret_cast<int*>(p);
+  a.part_q = reinterpret_cast<float*>(p + 256);
+  a.part_c = reinterpret_cast<int32_t*>(p + 256 + m);
+  a.part_n = reinterpret_cast<int32_t*>(p + 256 + 2 * m);
+  a.part_err = reinterpret_cast<int32_t*>(p + 256 + 2 * m + align_up(slots * 4, 256));
+  a.loss = loss, a.counts = counts, a.prob = prob, a.coef = coef;
+  if (a.chunks) {
+    const int st = dtype == MOE_F32   ? launch_partial<float>(a, V, s)
+                   : dtype == MOE_F16 ? launch_partial<__half>(a, V, s)
+                                      : launch_partial<__nv_bfloat16>(a, V, s);
+    if (st != MOE_OK) return st;
+  }
+  // columns of a CTA and threads of a column, powers of two: as many threads
+  // as a sequence has slots, on average
+  int cols = 8;
+  while (cols * kFinCluster < E) cols *= 2;
+  int w = 1;
+  while (w * cols < kFinThreads && w < a.chunks / (S > 0 ? S : 1) + 1) w *= 2;
+  return launch_pdl(__func__, balance_finish_kernel, dim3(kFinCluster), dim3(kFinThreads), 0, s, a, cols, w);
+}
+
+int launch_router_backward(const void* logits, int dtype, const int32_t* idx, const float* d_w, int T, int E, int k,
+                           int renorm, const int32_t* off, int S, const uint8_t* mask, const int32_t* counts,
+                           const float* coef, const float* d_loss, void* out, int out_dtype, cudaStream_t s) {
+  if (T == 0) return MOE_OK;
+  RouterGradArgs a{};
+  const int V = values_for(E);
+  a.logits = logits, a.idx = idx, a.d_w = d_w, a.T = T, a.E = E, a.k = k, a.renorm = renorm, a.off = off, a.S = S;
+  a.mask = mask, a.counts = counts, a.coef = coef, a.d_loss = d_loss, a.out = out;
+  a.L = lanes_for(E, V);
+  a.vec = E % 4 == 0;
+  const int groups = kBalThreads / a.L;
+  const int blocks = num_sms() * 8;
+  a.chunk = (T + blocks - 1) / blocks;
+  a.chunk = (a.chunk + groups - 1) / groups * groups;
+  const int grid = (T + a.chunk - 1) / a.chunk;
+  if (dtype == MOE_F32) return launch_grad_to<float>(a, out_dtype, V, grid, s);
+  if (dtype == MOE_F16) return launch_grad_to<__half>(a, out_dtype, V, grid, s);
+  return launch_grad_to<__nv_bfloat16>(a, out_dtype, V, grid, s);
+}
+
+}  // namespace moe

@@ -113,7 +113,132 @@ __global__ void __launch_bounds__(kCombThreads) combine_kernel(const __nv_bfloat
   if (p1) store8(o + c1, a1);
 }
 
+// ---------------------------------------------------------------- gradient
+//   dY[token_to_row[t, j]] = w[t, j] * dout[t],   dY[R + t] = dout[t] (shared),
+//   dw[t, j] = <Y[token_to_row[t, j]], dout[t]>.
+// Bound by memory: dout once, k rows of Y, k (+ 1) rows of dY.  One CTA a
+// token, so that dout's row is read once and stays in registers while the k
+// rows pass by it; each thread walks 16-byte pieces with eight rows in flight.
+constexpr int kCombGradSlots = 8;
+
+__device__ __forceinline__ void load_grad(const __nv_bfloat16* p, float (&g)[8]) {
+  unpack8(__ldg(reinterpret_cast<const uint4*>(p)), g);
+}
+__device__ __forceinline__ void load_grad(const float* p, float (&g)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w, g[4] = b.x, g[5] = b.y, g[6] = b.z, g[7] = b.w;
+}
+
+// S: slots of one sweep over the columns (1, 2, 4 or 8); more slots take more sweeps
+template <typename GT, int S>
+__global__ void __launch_bounds__(256) combine_backward_kernel(
+    const GT* __restrict__ dout, const __nv_bfloat16* __restrict__ Y, const int32_t* __restrict__ t2r,
+    const float* __restrict__ w, int has_shared, int T, int d, int k, const int32_t* __restrict__ shared_base,
+    __nv_bfloat16* __restrict__ dY, float* __restrict__ dw) {
+  pdl_wait();
+  pdl_launch_dependents();
+  __shared__ float s_dot[8][S];
+  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long long rows = static_cast<long long>(T) * (k + (has_shared ? 1 : 0));
+  const GT* g_row = dout + static_cast<size_t>(t) * d;
+  __nv_bfloat16* shared_row = nullptr;
+  if (has_shared && dY) {
+    const long long r = (shared_base ? static_cast<long long>(__ldg(shared_base)) : static_cast<long long>(T) * k) + t;
+    if (r >= 0 && r < rows) shared_row = dY + r * d;
+  }
+  for (int j0 = 0; j0 < k; j0 += S) {
+    const int n = min(S, k - j0);
+    long long row[S];
+    float wj[S], dot[S];
+#pragma unroll
+    for (int u = 0; u < S; ++u) {
+      row[u] = u < n ? __ldg(t2r + static_cast<size_t>(t) * k + j0 + u) : -1;
+      if (row[u] >= rows) row[u] = -1;
+      wj[u] = u < n ? __ldg(w + static_cast<size_t>(t) * k + j0 + u) : 0.f;
+      dot[u] = 0.f;
+    }
+    for (int c = tid * 8; c < d; c += blockDim.x * 8) {
+      float g[8];
+      load_grad(g_row + c, g);
+      if (dw) {
+        uint4 y[S];
+#pragma unroll
+        for (int u = 0; u < S; ++u)
+          y[u] = row[u] >= 0 ? __ldg(reinterpret_cast<const uint4*>(Y + row[u] * d + c)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int u = 0; u < S; ++u) {
+          float f[8];
+          unpack8(y[u], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot[u] = fmaf(f[i], g[i], dot[u]);
+        }
+      }
+      if (dY) {
+#pragma unroll
+        for (int u = 0; u < S; ++u) {
+          if (row[u] < 0) continue;
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = wj[u] * g[i];
+          store8(dY + row[u] * d + c, v);
+        }
+        if (shared_row && j0 == 0) store8(shared_row + c, g);
+      }
+    }
+    if (!dw) continue;
+#pragma unroll
+    for (int u = 0; u < S; ++u)
+      for (int o = 16; o; o >>= 1) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
+    if (lane == 0) {
+#pragma unroll
+      for (int u = 0; u < S; ++u) s_dot[warp][u] = dot[u];
+    }
+    __syncthreads();
+    if (tid < n) {
+      float all = 0.f;
+      for (int v = 0; v < static_cast<int>(blockDim.x) / 32; ++v) all += s_dot[v][tid];
+      // a slot without a row reached nothing, whatever dout holds
+      const int r = __ldg(t2r + static_cast<size_t>(t) * k + j0 + tid);
+      dw[static_cast<size_t>(t) * k + j0 + tid] = r >= 0 && r < rows ? all : 0.f;
+    }
+    __syncthreads();
+  }
+}
+
+template <typename GT>
+int launch_combine_grad(const GT* dout, const __nv_bfloat16* y, const int32_t* t2r, const float* w, int has_shared,
+                        int T, int d, int k, const int32_t* shared_base, __nv_bfloat16* dy, float* dw,
+                        cudaStream_t s) {
+  // a thread's share is one or more 16-byte pieces; narrow rows take fewer threads
+  const dim3 grid(T), block(d <= 256 ? 32 : d <= 1024 ? 128 : 256);
+  const char* where = "combine_backward_kernel";
+  if (k == 1)
+    return launch_pdl(where, combine_backward_kernel<GT, 1>, grid, block, 0, s, dout, y, t2r, w, has_shared, T, d, k,
+                      shared_base, dy, dw);
+  if (k == 2)
+    return launch_pdl(where, combine_backward_kernel<GT, 2>, grid, block, 0, s, dout, y, t2r, w, has_shared, T, d, k,
+                      shared_base, dy, dw);
+  if (k <= 4)
+    return launch_pdl(where, combine_backward_kernel<GT, 4>, grid, block, 0, s, dout, y, t2r, w, has_shared, T, d, k,
+                      shared_base, dy, dw);
+  return launch_pdl(where, combine_backward_kernel<GT, kCombGradSlots>, grid, block, 0, s, dout, y, t2r, w, has_shared,
+                    T, d, k, shared_base, dy, dw);
+}
+
 }  // namespace
+
+int launch_combine_backward(const void* dout, int dout_dtype, const void* Y, const int32_t* t2r, const float* w,
+                            int has_shared, int T, int d, int k, const int32_t* shared_base, void* dY, float* dw,
+                            cudaStream_t s) {
+  if (T == 0) return MOE_OK;
+  const __nv_bfloat16* y = static_cast<const __nv_bfloat16*>(Y);
+  __nv_bfloat16* dy = static_cast<__nv_bfloat16*>(dY);
+  if (dout_dtype == MOE_F32)
+    return launch_combine_grad(static_cast<const float*>(dout), y, t2r, w, has_shared, T, d, k, shared_base, dy, dw,
+                               s);
+  return launch_combine_grad(static_cast<const __nv_bfloat16*>(dout), y, t2r, w, has_shared, T, d, k, shared_base, dy,
+                             dw, s);
+}
 
 int launch_combine(const void* Y, const int32_t* t2r, const float* w, int has_shared, int T, int d, int k,
                    void* out, int out_dtype, cudaStream_t s, const int32_t* shared_base) {

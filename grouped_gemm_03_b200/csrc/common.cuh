@@ -156,6 +156,46 @@ const char* gemm_variant_name(int variant);
 // slots that overflowed an expert's capacity and are skipped.
 int launch_combine(const void* Y, const int32_t* t2r, const float* w, int has_shared, int T, int d, int k,
                    void* out, int out_dtype, cudaStream_t s, const int32_t* shared_base = nullptr);
+// shared_base as for launch_combine; dY or dw may be nullptr (not wanted)
+int launch_combine_backward(const void* dout, int dout_dtype, const void* Y, const int32_t* t2r, const float* w,
+                            int has_shared, int T, int d, int k, const int32_t* shared_base, void* dY, float* dw,
+                            cudaStream_t s);
+
+// off: nullptr for one sequence of all tokens (S = 1)
+size_t balance_workspace_bytes(int T, int E, int S);
+int launch_balance_loss(const void* logits, int dtype, const int32_t* idx, int T, int E, int k, const int32_t* off,
+                        int S, const uint8_t* mask, float alpha, float* loss, int32_t* counts, float* prob,
+                        float* coef, void* ws, cudaStream_t s);
+int launch_router_backward(const void* logits, int dtype, const int32_t* idx, const float* d_w, int T, int E, int k,
+                           int renorm, const int32_t* off, int S, const uint8_t* mask, const int32_t* counts,
+                           const float* coef, const float* d_loss, void* out, int out_dtype, cudaStream_t s);
+
+size_t adapter_plan_workspace_bytes(int rows, int n);
+int launch_adapter_plan(const int32_t* adapter, int rows, int n, int32_t* offsets, int32_t* order, void* ws,
+                        cudaStream_t s);
+int launch_lora(const void* x, const void* A, const void* B, const float* scale, const int32_t* offsets,
+                const int32_t* order, int n, int rows, int d, int N, int R, const void* base, void* out, int out_dtype,
+                float* h_out, cudaStream_t s);
+struct LoraBackwardArgs {
+  const void* dC;
+  const void* x;
+  const float* h;
+  const void* A;
+  const void* B;
+  const float* scale;
+  const int32_t* offsets;
+  const int32_t* order;
+  int n, rows, d, N, R;
+  const void* dx_base;
+  void* dx;       // nullptr: not wanted; likewise dA, dB
+  int dx_dtype;
+  void* dA;
+  void* dB;
+  int grad_dtype;
+  void* ws;
+};
+size_t lora_backward_workspace_bytes(int rows, int n, int d, int N, int R);
+int launch_lora_backward(const LoraBackwardArgs& a, cudaStream_t s);
 // pow2: power-of-two (MX) block scales instead of amax / 448
 int launch_quantize_weights(const void* W, int G, int N, int K, uint8_t* Wq, float* scales, cudaStream_t s,
                             bool pow2 = false);

@@ -5,6 +5,7 @@
 #include <cstring>
 
 #include "common.cuh"
+#include "lora.cuh"
 
 namespace moe {
 
@@ -385,6 +386,139 @@ int moe_combine_plan(const void* Y, const int32_t* token_to_row, const float* to
   if (!aligned(Y, 16) || !aligned(out, 16)) return MOE_ERR_INVALID;
   return launch_combine(Y, token_to_row, topk_w, has_shared, T, d, k, out, out_dtype, as_stream(stream),
                         T > 0 ? offsets + E : nullptr);
+}
+
+int moe_combine_backward(const void* dout, int dout_dtype, const void* Y, const int32_t* token_to_row,
+                         const float* topk_w, const int32_t* offsets, int E, int has_shared, int T, int d, int k,
+                         void* dY, float* d_topk_w, void* stream) {
+  if (T < 0 || d <= 0 || k <= 0 || k > kMaxTopK) return MOE_ERR_INVALID;
+  if (offsets && (E <= 0 || E > kMaxExperts)) return MOE_ERR_INVALID;
+  if (static_cast<long long>(T) * (k + 1) > kMaxPermuteRows) return MOE_ERR_UNSUPPORTED;
+  if (d % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  if (dout_dtype != MOE_F32 && dout_dtype != MOE_BF16) return MOE_ERR_INVALID;
+  if (!dY && !d_topk_w && T > 0) return MOE_ERR_INVALID;
+  if (T > 0 && (!dout || !token_to_row || !topk_w || (d_topk_w && !Y))) return MOE_ERR_INVALID;
+  if (T > 0 && dY && (dY == Y || dY == dout)) return MOE_ERR_INVALID;
+  if (!aligned(dout, 16) || !aligned(Y, 16) || !aligned(dY, 16)) return MOE_ERR_INVALID;
+  return launch_combine_backward(dout, dout_dtype, Y, token_to_row, topk_w, has_shared, T, d, k,
+                                 offsets ? offsets + E : nullptr, dY, d_topk_w, as_stream(stream));
+}
+
+// ------------------------------------------------------------------ training the router
+namespace {
+bool logits_dtype(int dt) { return dt == MOE_F16 || dt == MOE_F32 || dt == MOE_BF16; }
+
+// shapes the balance loss and the router's gradient share
+int check_router_shape(int T, int E, int k, int S, const int32_t* seq_offsets) {
+  if (T < 0 || E <= 0 || k <= 0 || k > E || k > kMaxTopK || E > kMaxExperts || S <= 0) return MOE_ERR_INVALID;
+  if (!seq_offsets && S != 1) return MOE_ERR_INVALID;
+  if (static_cast<long long>(T) * (k + 1) > kMaxPermuteRows || S > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+}  // namespace
+
+size_t moe_balance_loss_workspace_size(int T, int E, int S) {
+  if (T < 0 || E <= 0 || S <= 0) return 0;
+  return balance_workspace_bytes(T, E, S);
+}
+
+int moe_balance_loss(const void* logits, int dtype, const int32_t* topk_idx, int T, int E, int k,
+                     const int32_t* seq_offsets, int S, const uint8_t* token_mask, float alpha, float* loss,
+                     int32_t* counts, float* prob, float* coef, void* ws, size_t ws_bytes, void* stream) {
+  const int st = check_router_shape(T, E, k, S, seq_offsets);
+  if (st != MOE_OK) return st;
+  if (!logits_dtype(dtype)) return MOE_ERR_INVALID;
+  if (!loss || !counts || !coef) return MOE_ERR_INVALID;
+  if (T > 0 && (!logits || !topk_idx)) return MOE_ERR_INVALID;
+  if (!aligned(logits, 16)) return MOE_ERR_INVALID;
+  if (!ws || !aligned(ws, 256)) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < moe_balance_loss_workspace_size(T, E, S)) return MOE_ERR_WORKSPACE;
+  return launch_balance_loss(logits, dtype, topk_idx, T, E, k, seq_offsets, S, token_mask, alpha, loss, counts, prob,
+                             coef, ws, as_stream(stream));
+}
+
+int moe_router_backward(const void* logits, int dtype, const int32_t* topk_idx, const float* d_topk_w, int T, int E,
+                        int k, int renormalize, const int32_t* seq_offsets, int S, const uint8_t* token_mask,
+                        const int32_t* counts, const float* coef, const float* d_loss, void* d_logits, int d_dtype,
+                        void* stream) {
+  const int st = check_router_shape(T, E, k, S, seq_offsets);
+  if (st != MOE_OK) return st;
+  if (!logits_dtype(dtype) || !logits_dtype(d_dtype)) return MOE_ERR_INVALID;
+  if ((counts == nullptr) != (coef == nullptr)) return MOE_ERR_INVALID;
+  if (T > 0 && !d_topk_w && !counts) return MOE_ERR_INVALID;
+  if (T > 0 && (!logits || !topk_idx || !d_logits)) return MOE_ERR_INVALID;
+  if (T > 0 && d_logits == logits && d_dtype != dtype) return MOE_ERR_INVALID;
+  if (!aligned(logits, 16) || !aligned(d_logits, 16)) return MOE_ERR_INVALID;
+  return launch_router_backward(logits, dtype, topk_idx, d_topk_w, T, E, k, renormalize, seq_offsets, S, token_mask,
+                                counts, coef, d_loss, d_logits, d_dtype, as_stream(stream));
+}
+
+// ------------------------------------------------------------------ adapters
+namespace {
+int check_adapter_shape(int n, int rows, int d, int N, int R) {
+  if (n <= 0 || rows < 0 || d <= 0 || N <= 0 || R <= 0) return MOE_ERR_INVALID;
+  if (n > kMaxAdapters || rows > kMaxPermuteRows) return MOE_ERR_UNSUPPORTED;
+  if (R % 8 != 0 || R > kMaxRank || d % 8 != 0 || N % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+}  // namespace
+
+size_t moe_adapter_plan_workspace_size(int rows, int n) {
+  if (rows < 0 || n <= 0) return 0;
+  return adapter_plan_workspace_bytes(rows, n);
+}
+
+int moe_adapter_plan(const int32_t* row_adapter, int rows, int n, int32_t* offsets, int32_t* order, void* ws,
+                     size_t ws_bytes, void* stream) {
+  if (n <= 0 || rows < 0) return MOE_ERR_INVALID;
+  if (n > kMaxAdapters || rows > kMaxPermuteRows) return MOE_ERR_UNSUPPORTED;
+  if (!offsets || (rows > 0 && (!row_adapter || !order))) return MOE_ERR_INVALID;
+  if (!ws || !aligned(ws, 256)) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < moe_adapter_plan_workspace_size(rows, n)) return MOE_ERR_WORKSPACE;
+  return launch_adapter_plan(row_adapter, rows, n, offsets, order, ws, as_stream(stream));
+}
+
+int moe_lora(const void* x, const void* A, const void* B, const float* scale, const int32_t* offsets,
+             const int32_t* order, int n, int rows, int d, int N, int R, const void* base, void* out, int out_dtype,
+             float* h_out, void* stream) {
+  const int st = check_adapter_shape(n, rows, d, N, R);
+  if (st != MOE_OK) return st;
+  if (out_dtype != MOE_F32 && out_dtype != MOE_BF16) return MOE_ERR_INVALID;
+  if (!A || !B || !offsets) return MOE_ERR_INVALID;
+  if (rows > 0 && (!x || !order || !out || out == x)) return MOE_ERR_INVALID;
+  if (!aligned(x, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(base, 16) || !aligned(out, 16) ||
+      !aligned(h_out, 16))
+    return MOE_ERR_INVALID;
+  return launch_lora(x, A, B, scale, offsets, order, n, rows, d, N, R, base, out, out_dtype, h_out,
+                     as_stream(stream));
+}
+
+size_t moe_lora_backward_workspace_size(int rows, int n, int d, int N, int R) {
+  if (check_adapter_shape(n, rows, d, N, R) != MOE_OK) return 0;
+  return lora_backward_workspace_bytes(rows, n, d, N, R);
+}
+
+int moe_lora_backward(const void* dC, const void* x, const float* h, const void* A, const void* B, const float* scale,
+                      const int32_t* offsets, const int32_t* order, int n, int rows, int d, int N, int R,
+                      const void* dx_base, void* dx, int dx_dtype, void* dA, void* dB, int grad_dtype, void* ws,
+                      size_t ws_bytes, void* stream) {
+  const int st = check_adapter_shape(n, rows, d, N, R);
+  if (st != MOE_OK) return st;
+  if (dx_dtype != MOE_F32 && dx_dtype != MOE_BF16) return MOE_ERR_INVALID;
+  if (grad_dtype != MOE_F32 && grad_dtype != MOE_BF16) return MOE_ERR_INVALID;
+  if (!A || !B || !offsets || (rows > 0 && !dx && !dA && !dB)) return MOE_ERR_INVALID;
+  if (rows > 0 && (!dC || !x || !h || !order)) return MOE_ERR_INVALID;
+  if (rows > 0 && dx && (dx == dC || dx == x)) return MOE_ERR_INVALID;
+  if (!aligned(dC, 16) || !aligned(x, 16) || !aligned(h, 16) || !aligned(A, 16) || !aligned(B, 16) ||
+      !aligned(dx_base, 16) || !aligned(dx, 16) || !aligned(dA, 16) || !aligned(dB, 16))
+    return MOE_ERR_INVALID;
+  if (!ws || !aligned(ws, 256)) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < lora_backward_workspace_bytes(rows, n, d, N, R)) return MOE_ERR_WORKSPACE;
+  LoraBackwardArgs a{};
+  a.dC = dC, a.x = x, a.h = h, a.A = A, a.B = B, a.scale = scale, a.offsets = offsets, a.order = order;
+  a.n = n, a.rows = rows, a.d = d, a.N = N, a.R = R;
+  a.dx_base = dx_base, a.dx = dx, a.dx_dtype = dx_dtype, a.dA = dA, a.dB = dB, a.grad_dtype = grad_dtype, a.ws = ws;
+  return launch_lora_backward(a, as_stream(stream));
 }
 
 // ------------------------------------------------------------------ FP8 weights

@@ -298,6 +298,125 @@ int moe_combine(const void* Y, const int32_t* token_to_row, const float* topk_w,
 int moe_combine_plan(const void* Y, const int32_t* token_to_row, const float* topk_w, const int32_t* offsets, int E,
                      int has_shared, int T, int d, int k, void* out, int out_dtype, void* stream);
 
+/* Gradient of moe_combine / moe_combine_plan:
+ *   dY[token_to_row[t,j]] = topk_w[t,j] * dout[t],  dY[R + t] = dout[t] (if has_shared),
+ *   d_topk_w[t,j] = sum_c Y[token_to_row[t,j], c] * dout[t, c]   (fp32 sums).
+ *   dout [T, d] dout_dtype (MOE_BF16 | MOE_F32);  Y [R', d] MOE_BF16 as moe_combine read it
+ *   offsets: the permute's DEVICE array with E experts, when the plan has a
+ *       capacity (the shared rows then start at offsets[E]), else NULL (E unused)
+ *   dY [R', d] MOE_BF16 or NULL (not wanted);  d_topk_w [T, k] fp32 or NULL; one of the two is given.
+ *       Y may be NULL when d_topk_w is.
+ * A slot with token_to_row[t,j] < 0 (or past R' = T*k (+ T)) writes no row of
+ * dY and has d_topk_w = 0; rows of dY that belong to no token are left as
+ * they were.  dY must not overlap Y or dout.  d % 8 == 0; dout, Y and dY
+ * 16-byte aligned. */
+int moe_combine_backward(const void* dout, int dout_dtype, const void* Y, const int32_t* token_to_row,
+                         const float* topk_w, const int32_t* offsets, int E, int has_shared, int T, int d, int k,
+                         void* dY, float* d_topk_w, void* stream);
+
+/* ---------------------------------------------------------------- training the router
+ * Balance loss with per-expert counts ("MegaMoE ..." §2: alpha * E * sum_i
+ * f_i P_i), taken per sequence and averaged over the sequences that have
+ * tokens.  With p = softmax(logits), sequence s = tokens seq_offsets[s] ..
+ * seq_offsets[s+1]-1 that the mask keeps, N_s of them:
+ *   counts[s,e] = the (token, slot) pairs with topk_idx = e
+ *   prob[s,e]   = mean of p_e over the sequence's tokens (0 if it has none)
+ *   coef[s]     = alpha * E / (k * N_s^2 * S'), S' = sequences with tokens (0 if it has none)
+ *   loss        = sum_s coef[s] * N_s * sum_e counts[s,e] * prob[s,e]
+ *               = mean_s alpha * E * sum_e (counts / (k N_s)) * prob
+ *   logits      [T, E] dtype MOE_F32 | MOE_F16 | MOE_BF16 (moe_router_topk's logits_out, say).
+ *               A logit of -inf has probability 0; a token whose logits are all -inf adds
+ *               none to prob.  What a token that does not count holds is not read.
+ *   topk_idx    [T, k] int32; -1 is a slot without an expert (not counted)
+ *   seq_offsets [S+1] int32 DEVICE array, seq_offsets[0] = 0, non-decreasing,
+ *               <= T; tokens from seq_offsets[S] on belong to no sequence.
+ *               NULL: one sequence of all T tokens (S = 1).
+ *   token_mask  [T] uint8 or NULL: 0 leaves a token out (padding)
+ *   loss [1], prob [S, E] (or NULL), coef [S] fp32; counts [S, E] int32
+ *   ws          moe_balance_loss_workspace_size(T, E, S) bytes (status + partial sums)
+ * Status word: MOE_ERR_BAD_OFFSETS for bad seq_offsets, MOE_ERR_INVALID for an
+ * id outside -1 .. E-1 (not counted).  Two launches; sums run in a fixed order.
+ * E <= 1024, k <= min(E, 32), T * (k + 1) <= 2^30, S <= 2^20. */
+size_t moe_balance_loss_workspace_size(int T, int E, int S);
+int moe_balance_loss(const void* logits, int dtype, const int32_t* topk_idx, int T, int E, int k,
+                     const int32_t* seq_offsets, int S, const uint8_t* token_mask, float alpha, float* loss,
+                     int32_t* counts, float* prob, float* coef, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of the router's logits in one pass: from the gate weights'
+ * gradient d_topk_w (moe_combine_backward's), from the balance loss, or from
+ * both.  With p = softmax(logits) and c = counts of the token's sequence:
+ *   raw gates (renormalize = 0, w_j = p[topk_idx_j]) and the balance loss:
+ *     G_e = sum_{j: topk_idx_j = e} d_topk_w_j + d_loss * coef[s] * c_e
+ *     d_logits_e = p_e * (G_e - sum_i G_i p_i)
+ *   renormalised gates (w_j = p_j / sum_S p) add, for each selected expert,
+ *     w_j * (d_topk_w_j - sum_S w d_topk_w)
+ *   logits, topk_idx, seq_offsets, S, token_mask  as for moe_balance_loss (ids
+ *               outside 0 .. E-1 select nothing)
+ *   d_topk_w    [T, k] fp32, or NULL: no gradient through the gates
+ *   counts, coef  as moe_balance_loss wrote them, both or neither (NULL: no balance
+ *               loss; seq_offsets and token_mask are then not read)
+ *   d_loss      DEVICE fp32 scalar, the loss's own gradient, or NULL (1)
+ *   d_logits    [T, E] d_dtype MOE_F32 | MOE_F16 | MOE_BF16.  A row that neither part
+ *               reaches (no balance loss for the token, d_topk_w all 0) is 0 whatever its logits hold.
+ * Limits as for moe_balance_loss.  d_logits may be logits itself when the
+ * types are equal, and must not overlap it otherwise. */
+int moe_router_backward(const void* logits, int dtype, const int32_t* topk_idx, const float* d_topk_w, int T, int E,
+                        int k, int renormalize, const int32_t* seq_offsets, int S, const uint8_t* token_mask,
+                        const int32_t* counts, const float* coef, const float* d_loss, void* d_logits, int d_dtype,
+                        void* stream);
+
+/* ---------------------------------------------------------------- adapters
+ * Low-rank adapters of many requests beside one projection (a shared expert's,
+ * a dense layer's, or, with one adapter per (request, expert), an expert's
+ * rows): each row of the batch takes its own adapter, or none.
+ *
+ * The plan orders a batch's rows by adapter; every projection of the batch
+ * shares it.
+ *   row_adapter [rows] int32: the row's adapter, 0 .. n-1, or -1 for none
+ *   offsets     [n+1] int32: adapter a's rows are order[offsets[a]] .. order[offsets[a+1]-1],
+ *               ascending; the rows without an adapter follow from offsets[n] on
+ *   order       [rows] int32
+ *   ws          moe_adapter_plan_workspace_size(rows, n) bytes (status + counts)
+ * An id outside -1 .. n-1 counts as none and sets MOE_ERR_INVALID in the
+ * status word.  1 <= n <= 1024, rows <= 2^30. */
+size_t moe_adapter_plan_workspace_size(int rows, int n);
+int moe_adapter_plan(const int32_t* row_adapter, int rows, int n, int32_t* offsets, int32_t* order, void* ws,
+                     size_t ws_bytes, void* stream);
+
+/* out[r] = base[r] + scale[a] * (x[r] A[a]^T) B[a]^T for the rows of adapter a,
+ * out[r] = base[r] for the rows without one; one launch.
+ *   x      [rows, d] MOE_BF16;  A [n, R, d], B [n, N, R] MOE_BF16;  scale [n] fp32 or NULL (1)
+ *   offsets, order  the plan (DEVICE arrays; entries outside their range are
+ *          skipped, nothing outside the buffers is read or written)
+ *   base   [rows, N] out_dtype, the projection's output (moe_grouped_gemm's C), or NULL (0)
+ *   out    [rows, N] out_dtype (MOE_BF16 | MOE_F32); may be base itself: the
+ *          rows without an adapter are then not touched
+ *   h_out  [rows, R] fp32: x A^T (0 for rows without an adapter), which
+ *          moe_lora_backward takes, or NULL
+ * fp32 sums, rounded once to out_dtype.  R a multiple of 8, 8 <= R <= 128
+ * (pad smaller ranks with zeros); d % 8 == 0, N % 8 == 0; x, A, B, base, out
+ * and h_out 16-byte aligned; out must not overlap x. */
+int moe_lora(const void* x, const void* A, const void* B, const float* scale, const int32_t* offsets,
+             const int32_t* order, int n, int rows, int d, int N, int R, const void* base, void* out, int out_dtype,
+             float* h_out, void* stream);
+
+/* Gradient of moe_lora, from dC = d out and the h that the forward kept:
+ *   dh[r] = scale[a] * dC[r] B[a]
+ *   dx[r] = dx_base[r] + dh[r] A[a]   (dx_base[r] alone for rows without an adapter)
+ *   dA[a] = sum_r dh[r]^T x[r],  dB[a] = scale[a] * sum_r dC[r]^T h[r]   (0 for an adapter without rows)
+ *   dC [rows, N], x [rows, d] MOE_BF16;  h [rows, R] fp32;  A, B, scale, offsets, order as for moe_lora
+ *   dx_base [rows, d] dx_dtype (the projection's own input gradient) or NULL (0)
+ *   dx      [rows, d] dx_dtype (MOE_BF16 | MOE_F32) or NULL (not wanted); may be dx_base itself
+ *   dA [n, R, d], dB [n, N, R] grad_dtype (MOE_F32 | MOE_BF16), each or NULL; one of dx, dA, dB is given
+ *   ws      moe_lora_backward_workspace_size(...) bytes (dh and partial sums; no status word)
+ * Sums run in a fixed order.  Shapes and alignment as for moe_lora; dx must
+ * not overlap dC or x. */
+size_t moe_lora_backward_workspace_size(int rows, int n, int d, int N, int R);
+int moe_lora_backward(const void* dC, const void* x, const float* h, const void* A, const void* B, const float* scale,
+                      const int32_t* offsets, const int32_t* order, int n, int rows, int d, int N, int R,
+                      const void* dx_base, void* dx, int dx_dtype, void* dA, void* dB, int grad_dtype, void* ws,
+                      size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- FP8 weights
  * Quantise bf16 weights W [G, N, K] per 128x128 block ("MegaMoE ..." §2.3,
  * §5.1): s = amax(block)/448 (1 if the block is zero), Wq = e4m3_rn_satfinite(W/s).
