@@ -11,7 +11,6 @@ Build the library with ``python -m grouped_gemm_03_b200.build``.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from dataclasses import dataclass
 
@@ -317,113 +316,131 @@ def combine(Y, token_to_row, topk_w, has_shared: bool, out_dtype=torch.bfloat16,
     return o
 
 
-def _held(device, t, what: str, dtypes, shape):
-    """The address of a tensor the call reads or writes (None stays None), checked: contiguous, on the current
+_F32, _I32, _BF16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
+_ACT = (torch.bfloat16, torch.float32)
+_LOGITS = (torch.float32, torch.float16, torch.bfloat16)
+_MASK = (torch.uint8, torch.bool)
+
+
+def _device(t) -> int:
+    """The device of a call's first tensor, which has to be the current one: kernels launch there."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be contiguous CUDA tensors")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{torch._C._cuda_getDevice()}")
+    return dev
+
+
+def _held(dev, t, what: str, dtypes, shape):
+    """The address of a tensor the call reads or writes (None stays None), checked: contiguous, on the call's
     device, of one of these types and of this shape."""
     if t is None:
         return None
-    if not t.is_cuda or not t.is_contiguous():
+    if t.get_device() != dev or t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
+        if t.get_device() != dev:
+            raise ValueError(f"{what}: every tensor of a call must be a CUDA tensor on one device (cuda:{dev})")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{what}: unsupported dtype {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{what}: shape {tuple(t.shape)} where {tuple(shape)} is wanted")
         raise ValueError(f"{what}: tensors must be contiguous CUDA tensors")
-    if t.get_device() != device:
-        raise ValueError(f"{what} is on cuda:{t.get_device()}, the current device is cuda:{device}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{what}: unsupported dtype {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{what}: shape {tuple(t.shape)} where {tuple(shape)} is wanted")
     return t.data_ptr()
 
 
-_F32, _I32, _BF16, _U8 = (torch.float32,), (torch.int32,), (torch.bfloat16,), (torch.uint8,)
-_ACT = (torch.bfloat16, torch.float32)
-_LOGITS = (torch.float32, torch.float16, torch.bfloat16)
-
-
-def _workspace(ws, nbytes: int, dev: int):
-    """(address, bytes) of the caller's workspace, or of a new one, and the tensor that keeps it."""
+def _workspace(like, ws, nbytes: int):
+    """The caller's workspace, or a new one of this size, beside `like`."""
     if ws is None:
-        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-    elif not ws.is_cuda or ws.get_device() != dev or not ws.is_contiguous():
-        raise ValueError("ws: a contiguous tensor on the current CUDA device is wanted")
-    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+        return like.new_empty(max(nbytes, 256), dtype=torch.uint8)
+    if ws.get_device() != like.get_device() or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError("ws: a contiguous uint8 tensor on the call's device is wanted")
+    return ws
 
 
-def _on_stream(f):
-    """`stream=`: run the call with that stream current, so that the tensors it allocates belong to it."""
-    @functools.wraps(f)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return f(*args, **kw)
-        with torch.cuda.stream(stream):
-            return f(*args, **kw)
-    return call
+_stream_of = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
 
 
-def _current(dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev)
-
-
-@_on_stream
 def combine_backward(dout, Y, token_to_row, topk_w, has_shared: bool, offsets=None, want_dY: bool = True,
-                     want_dw: bool = True, dY=None):
+                     want_dw: bool = True, dY=None, stream=None):
     """(dY [R', d] bf16, d_topk_w [T, k] fp32) of combine's output gradient (moe_combine_backward).
 
     offsets: the permute's, for a plan with a capacity.  Either result can be left out (None); Y may be
     None without d_topk_w.  Rows of dY that belong to no token are left as they were (a new dY's are 0)."""
-    dev = torch.cuda.current_device()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return combine_backward(dout, Y, token_to_row, topk_w, has_shared, offsets, want_dY, want_dw, dY)
+    dev = _device(dout)
     T, k = token_to_row.shape
     d = dout.shape[1]
-    rows = T * k + (T if has_shared else 0)
+    rows = T * k + T if has_shared else T * k
     E = 0 if offsets is None else offsets.numel() - 1 - (1 if has_shared else 0)
     p_dout = _held(dev, dout, "dout", _ACT, (T, d))
     p_t2r = _held(dev, token_to_row, "token_to_row", _I32, (T, k))
     p_w = _held(dev, topk_w, "topk_w", _F32, (T, k))
     p_off = _held(dev, offsets, "offsets", _I32, (E + 1 + (1 if has_shared else 0),))
     p_Y = _held(dev, Y, "Y", _BF16, (rows, d))
-    if want_dY and dY is None:
-        dY = (torch.empty if offsets is None else torch.zeros)((rows, d), dtype=torch.bfloat16, device=dev)
-    dw = torch.empty((T, k), dtype=torch.float32, device=dev) if want_dw else None
-    p_dY = _held(dev, dY, "dY", _BF16, (rows, d)) if want_dY else None
-    _check(lib().moe_combine_backward(p_dout, _TORCH_DT[dout.dtype], p_Y, p_t2r, p_w, p_off, E, int(has_shared), T, d,
-                                      k, p_dY, None if dw is None else dw.data_ptr(), _current(dev)),
-           "moe_combine_backward")
-    return (dY if want_dY else None), dw
+    if not want_dY:
+        dY = None
+    elif dY is None:
+        if offsets is not None:
+            dY = dout.new_zeros((rows, d), dtype=torch.bfloat16)
+        else:
+            dY = dout.new_empty((rows, d), dtype=torch.bfloat16) if Y is None else torch.empty_like(Y)
+    dw = torch.empty_like(topk_w) if want_dw else None
+    st = lib().moe_combine_backward(p_dout, _TORCH_DT[dout.dtype], p_Y, p_t2r, p_w, p_off, E, has_shared, T, d, k,
+                                    _held(dev, dY, "dY", _BF16, (rows, d)), dw.data_ptr() if want_dw else None,
+                                    _stream_of(dev))
+    _check(st, "moe_combine_backward")
+    return dY, dw
 
 
 # ---------------------------------------------------------------- training the router
-@_on_stream
-def balance_loss(logits, topk_idx, alpha: float, seq_offsets=None, mask=None, want_prob: bool = True, ws=None):
+def balance_loss(logits, topk_idx, alpha: float, seq_offsets=None, mask=None, want_prob: bool = True, ws=None,
+                 stream=None):
     """(loss [1] fp32, counts [S, E] int32, prob [S, E] fp32 or None, coef [S] fp32) of moe_balance_loss.
 
     seq_offsets [S+1] int32 (None: one sequence of all tokens); mask [T] uint8 or bool, 0 for padding.
     counts and coef go to router_backward.  Bad ids or offsets show in the status word of a caller's `ws`
     (read_device_status)."""
-    dev = torch.cuda.current_device()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return balance_loss(logits, topk_idx, alpha, seq_offsets, mask, want_prob, ws)
+    dev = _device(logits)
     T, E = logits.shape
     k = topk_idx.shape[1]
     S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+    if S < 1:
+        raise ValueError("seq_offsets: at least two entries are wanted")
     p_l = _held(dev, logits, "logits", _LOGITS, (T, E))
     p_i = _held(dev, topk_idx, "topk_idx", _I32, (T, k))
     p_o = _held(dev, seq_offsets, "seq_offsets", _I32, (S + 1,))
-    p_m = _held(dev, mask, "mask", (torch.uint8, torch.bool), (T,))
+    p_m = _held(dev, mask, "mask", _MASK, (T,))
     L = lib()
-    p_ws, n_ws, ws = _workspace(ws, L.moe_balance_loss_workspace_size(T, E, S), dev)
-    loss = torch.empty(1, dtype=torch.float32, device=dev)
-    counts = torch.empty((max(S, 0), E), dtype=torch.int32, device=dev)
-    prob = torch.empty((max(S, 0), E), dtype=torch.float32, device=dev) if want_prob else None
-    coef = torch.empty(max(S, 0), dtype=torch.float32, device=dev)
-    _check(L.moe_balance_loss(p_l, _TORCH_DT[logits.dtype], p_i, T, E, k, p_o, S, p_m, alpha, loss.data_ptr(),
-                              counts.data_ptr(), prob.data_ptr() if want_prob else None, coef.data_ptr(), p_ws, n_ws,
-                              _current(dev)), "moe_balance_loss")
+    ws = _workspace(logits, ws, L.moe_balance_loss_workspace_size(T, E, S))
+    counts = topk_idx.new_empty((S, E))
+    # loss and coef share an allocation: the one is a row before the other's
+    both = logits.new_empty(S + 1, dtype=torch.float32)
+    loss, coef = both.split((1, S))
+    prob = logits.new_empty((S, E), dtype=torch.float32) if want_prob else None
+    p_both = both.data_ptr()
+    st = L.moe_balance_loss(p_l, _TORCH_DT[logits.dtype], p_i, T, E, k, p_o, S, p_m, alpha, p_both, counts.data_ptr(),
+                            prob.data_ptr() if want_prob else None, p_both + 4, ws.data_ptr(), ws.numel(),
+                            _stream_of(dev))
+    _check(st, "moe_balance_loss")
     return loss, counts, prob, coef
 
 
-@_on_stream
 def router_backward(logits, topk_idx, d_topk_w=None, renormalize: bool = False, counts=None, coef=None, d_loss=None,
-                    seq_offsets=None, mask=None, out_dtype=torch.float32, out=None):
+                    seq_offsets=None, mask=None, out_dtype=torch.float32, out=None, stream=None):
     """d_logits [T, E] of the gate weights' gradient and of the balance loss, either or both (moe_router_backward).
 
-    counts, coef: what balance_loss returned for the same seq_offsets and mask; d_loss: [1] fp32 or None (1)."""
-    dev = torch.cuda.current_device()
+    counts, coef: what balance_loss returned for the same seq_offsets and mask; d_loss: one fp32 value on the
+    device, or None (1)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return router_backward(logits, topk_idx, d_topk_w, renormalize, counts, coef, d_loss, seq_offsets, mask,
+                                   out_dtype, out)
+    dev = _device(logits)
     T, E = logits.shape
     k = topk_idx.shape[1]
     S = 1 if seq_offsets is None else seq_offsets.numel() - 1
@@ -431,42 +448,51 @@ def router_backward(logits, topk_idx, d_topk_w=None, renormalize: bool = False, 
     p_i = _held(dev, topk_idx, "topk_idx", _I32, (T, k))
     p_g = _held(dev, d_topk_w, "d_topk_w", _F32, (T, k))
     p_o = _held(dev, seq_offsets, "seq_offsets", _I32, (S + 1,))
-    p_m = _held(dev, mask, "mask", (torch.uint8, torch.bool), (T,))
+    p_m = _held(dev, mask, "mask", _MASK, (T,))
     p_n = _held(dev, counts, "counts", _I32, (S, E))
     p_c = _held(dev, coef, "coef", _F32, (S,))
-    p_d = _held(dev, None if d_loss is None else d_loss.reshape(1), "d_loss", _F32, (1,))
-    o = torch.empty((T, E), dtype=out_dtype, device=dev) if out is None else out
-    p_out = _held(dev, o, "out", _LOGITS, (T, E))
-    _check(lib().moe_router_backward(p_l, _TORCH_DT[logits.dtype], p_i, p_g, T, E, k, int(renormalize), p_o, S, p_m,
-                                     p_n, p_c, p_d, p_out, _TORCH_DT[o.dtype], _current(dev)),
-           "moe_router_backward")
-    return o
+    if d_loss is not None and d_loss.numel() != 1:
+        raise ValueError("d_loss: one value is wanted")
+    p_d = None if d_loss is None else _held(dev, d_loss, "d_loss", _F32, d_loss.shape)
+    if out is None:
+        out = torch.empty_like(logits, dtype=out_dtype)
+    st = lib().moe_router_backward(p_l, _TORCH_DT[logits.dtype], p_i, p_g, T, E, k, renormalize, p_o, S, p_m, p_n, p_c,
+                                   p_d, _held(dev, out, "out", _LOGITS, (T, E)), _TORCH_DT[out.dtype],
+                                   _stream_of(dev))
+    _check(st, "moe_router_backward")
+    return out
 
 
 # ---------------------------------------------------------------- adapters
-@_on_stream
-def adapter_plan(row_adapter, n: int, ws=None):
+def adapter_plan(row_adapter, n: int, ws=None, stream=None):
     """(offsets [n+1], order [rows]) int32: the rows in adapter order, those without one (-1) last
     (moe_adapter_plan).  Ids outside -1 .. n-1 count as none and show in the status word of a caller's `ws`."""
-    dev = torch.cuda.current_device()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return adapter_plan(row_adapter, n, ws)
+    dev = _device(row_adapter)
     rows = row_adapter.numel()
     p_r = _held(dev, row_adapter, "row_adapter", _I32, (rows,))
     L = lib()
-    p_ws, n_ws, ws = _workspace(ws, L.moe_adapter_plan_workspace_size(rows, n), dev)
-    offsets = torch.empty(max(n, 0) + 1, dtype=torch.int32, device=dev)
-    order = torch.empty(rows, dtype=torch.int32, device=dev)
-    _check(L.moe_adapter_plan(p_r, rows, n, offsets.data_ptr(), order.data_ptr(), p_ws, n_ws,
-                              _current(dev)), "moe_adapter_plan")
+    ws = _workspace(row_adapter, ws, L.moe_adapter_plan_workspace_size(rows, n))
+    offsets = row_adapter.new_empty(max(n, 0) + 1)
+    order = torch.empty_like(row_adapter)
+    st = L.moe_adapter_plan(p_r, rows, n, offsets.data_ptr(), order.data_ptr(), ws.data_ptr(), ws.numel(),
+                            _stream_of(dev))
+    _check(st, "moe_adapter_plan")
     return offsets, order
 
 
-@_on_stream
-def lora(x, A, B, offsets, order, scale=None, base=None, out_dtype=torch.bfloat16, out=None, want_h: bool = False):
+def lora(x, A, B, offsets, order, scale=None, base=None, out_dtype=torch.bfloat16, out=None, want_h: bool = False,
+         stream=None):
     """base + scale (x A^T) B^T, each row with its own adapter (moe_lora); with want_h also h = x A^T [rows, R] fp32.
 
     A [n, R, d], B [n, N, R] bf16; offsets, order: adapter_plan's; base [rows, N] or None (0).  out=base adds
     in place.  Without `out` the result has base's type, or out_dtype."""
-    dev = torch.cuda.current_device()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return lora(x, A, B, offsets, order, scale, base, out_dtype, out, want_h)
+    dev = _device(x)
     rows, d = x.shape
     n, R, _ = A.shape
     N = B.shape[1]
@@ -477,22 +503,28 @@ def lora(x, A, B, offsets, order, scale=None, base=None, out_dtype=torch.bfloat1
     p_ord = _held(dev, order, "order", _I32, (rows,))
     p_s = _held(dev, scale, "scale", _F32, (n,))
     if out is None:
-        out = torch.empty((rows, N), dtype=out_dtype if base is None else base.dtype, device=dev)
+        out = x.new_empty((rows, N), dtype=out_dtype) if base is None else torch.empty_like(base)
     p_out = _held(dev, out, "out", _ACT, (rows, N))
     p_base = _held(dev, base, "base", (out.dtype,), (rows, N))
-    h = torch.empty((rows, R), dtype=torch.float32, device=dev) if want_h else None
-    _check(lib().moe_lora(p_x, p_A, p_B, p_s, p_off, p_ord, n, rows, d, N, R, p_base, p_out, _TORCH_DT[out.dtype],
-                          h.data_ptr() if want_h else None, _current(dev)), "moe_lora")
+    h = x.new_empty((rows, R), dtype=torch.float32) if want_h else None
+    L = lib()
+    st = L.moe_lora(p_x, p_A, p_B, p_s, p_off, p_ord, n, rows, d, N, R, p_base, p_out, _TORCH_DT[out.dtype],
+                    h.data_ptr() if want_h else None, _stream_of(dev))
+    _check(st, "moe_lora")
     return (out, h) if want_h else out
 
 
-@_on_stream
 def lora_backward(dC, x, h, A, B, offsets, order, scale=None, dx_base=None, want_dx: bool = True,
-                  want_grads: bool = True, dx_dtype=torch.bfloat16, dx=None, grad_dtype=torch.float32, ws=None):
+                  want_grads: bool = True, dx_dtype=torch.bfloat16, dx=None, grad_dtype=torch.float32, ws=None,
+                  stream=None):
     """(dx [rows, d] or None, dA [n, R, d] or None, dB [n, N, R] or None) of lora's output gradient dC
     (moe_lora_backward).  h: what lora(..., want_h=True) kept; dx_base is added to dx and sets its type (dx=dx_base
     adds in place)."""
-    dev = torch.cuda.current_device()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return lora_backward(dC, x, h, A, B, offsets, order, scale, dx_base, want_dx, want_grads, dx_dtype, dx,
+                                 grad_dtype, ws)
+    dev = _device(dC)
     rows, d = x.shape
     n, R, _ = A.shape
     N = B.shape[1]
@@ -504,21 +536,25 @@ def lora_backward(dC, x, h, A, B, offsets, order, scale=None, dx_base=None, want
     p_off = _held(dev, offsets, "offsets", _I32, (n + 1,))
     p_ord = _held(dev, order, "order", _I32, (rows,))
     p_s = _held(dev, scale, "scale", _F32, (n,))
-    if want_dx and dx is None:
-        dx = torch.empty((rows, d), dtype=dx_dtype if dx_base is None else dx_base.dtype, device=dev)
-    p_dx = _held(dev, dx, "dx", _ACT, (rows, d)) if want_dx else None
-    p_base = _held(dev, dx_base, "dx_base", (dx.dtype,), (rows, d)) if want_dx else None
-    dA = dB = None
+    p_dx = p_base = dA = dB = None
+    dt = MOE_BF16
+    if not want_dx:
+        dx = None
+    else:
+        if dx is None:
+            dx = torch.empty_like(x, dtype=dx_dtype) if dx_base is None else torch.empty_like(dx_base)
+        p_dx = _held(dev, dx, "dx", _ACT, (rows, d))
+        p_base = _held(dev, dx_base, "dx_base", (dx.dtype,), (rows, d))
+        dt = _TORCH_DT[dx.dtype]
     if want_grads:
-        dA = torch.empty((n, R, d), dtype=grad_dtype, device=dev)
-        dB = torch.empty((n, N, R), dtype=grad_dtype, device=dev)
+        dA, dB = torch.empty_like(A, dtype=grad_dtype), torch.empty_like(B, dtype=grad_dtype)
     L = lib()
-    p_ws, n_ws, ws = _workspace(ws, L.moe_lora_backward_workspace_size(rows, n, d, N, R), dev)
-    _check(L.moe_lora_backward(p_dC, p_x, p_h, p_A, p_B, p_s, p_off, p_ord, n, rows, d, N, R, p_base, p_dx,
-                               _TORCH_DT[dx.dtype] if want_dx else MOE_BF16, dA.data_ptr() if want_grads else None,
-                               dB.data_ptr() if want_grads else None,
-                               _TORCH_DT[grad_dtype], p_ws, n_ws, _current(dev)), "moe_lora_backward")
-    return (dx if want_dx else None), dA, dB
+    ws = _workspace(x, ws, L.moe_lora_backward_workspace_size(rows, n, d, N, R))
+    st = L.moe_lora_backward(p_dC, p_x, p_h, p_A, p_B, p_s, p_off, p_ord, n, rows, d, N, R, p_base, p_dx, dt,
+                             dA.data_ptr() if want_grads else None, dB.data_ptr() if want_grads else None,
+                             _TORCH_DT[grad_dtype], ws.data_ptr(), ws.numel(), _stream_of(dev))
+    _check(st, "moe_lora_backward")
+    return dx, dA, dB
 
 
 # ---------------------------------------------------------------- FP8 weights

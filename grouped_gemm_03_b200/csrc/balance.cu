@@ -17,8 +17,8 @@
 //   w_j = p_j / sum_S p,   dlogit_{idx_j} += w_j (dw_j - sum_S w dw).
 //
 // Both kernels are bound by reading the logits (and writing their gradient):
-// one pass, each row held in registers by L lanes (4 columns a lane up to 128
-// experts, then 8, 16, 32), the softmax's maximum and sum by shuffles.
+// one pass, each row held in registers by L lanes of 8 columns (32 past 256
+// experts), the softmax's maximum and sum by shuffles.
 #include "common.cuh"
 
 namespace moe {
@@ -27,54 +27,89 @@ namespace {
 constexpr int kBalThreads = 256;
 constexpr int kBalMinChunk = 32;     // tokens of one block, at least
 constexpr int kBalMaxChunks = 592;   // blocks of the first pass: four on each of 148 SMs
+constexpr int kBalSmall = 512;       // tokens up to which one cluster does both passes
 constexpr int kFinThreads = 1024;
 constexpr int kFinCluster = 8;       // CTAs of the second pass, each a slice of the experts
 
-__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __half* p) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
-  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
-  return make_float4(a.x, a.y, b.x, b.y);
+// A row of E values over L lanes, V values a lane in pieces of C (16 bytes):
+// lane l holds columns (q * L + l) * C + c as value q * C + c.
+template <typename T>
+constexpr int piece() { return 16 / sizeof(T); }
+template <typename T>
+__device__ __forceinline__ int column(int i, int L, int l) {
+  return (i / piece<T>() * L + l) * piece<T>() + i % piece<T>();
 }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
-                     __uint_as_float(v.y & 0xffff0000u));
+
+__device__ __forceinline__ void unpack(const uint4& r, float (&f)[4], float) {
+  f[0] = __uint_as_float(r.x), f[1] = __uint_as_float(r.y), f[2] = __uint_as_float(r.z), f[3] = __uint_as_float(r.w);
 }
-__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(__half* p, float4 v) {
-  const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
-  *reinterpret_cast<uint2*>(p) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+__device__ __forceinline__ void unpack(const uint4& r, float (&f)[8], __half) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    f[2 * i] = v.x, f[2 * i + 1] = v.y;
+  }
 }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-  *reinterpret_cast<uint2*>(p) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+__device__ __forceinline__ void unpack(const uint4& r, float (&f)[8], __nv_bfloat16) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
 }
 __device__ __forceinline__ float from_f32(float v, float) { return v; }
 __device__ __forceinline__ __half from_f32(float v, __half) { return __float2half_rn(v); }
 __device__ __forceinline__ __nv_bfloat16 from_f32(float v, __nv_bfloat16) { return __float2bfloat16_rn(v); }
 
-// Lane l of the L lanes of a row holds columns (i * L + l) * 4 + c, c < 4, as v[4 * i + c].
+// A lane's share of a row as it lies in memory, so that the next rows' loads
+// can be in flight while this one is worked on.  vec: every row starts on 16
+// bytes and E fills whole pieces.
 template <typename T, int V>
-__device__ __forceinline__ void load_row(const T* row, int E, int L, int l, bool vec, bool live, float (&v)[V]) {
+struct Row {
+  uint4 raw[V / piece<T>()];
+  __device__ __forceinline__ void load(const T* row, int E, int L, int l, bool vec, bool live) {
+    constexpr int C = piece<T>();
 #pragma unroll
-  for (int i = 0; i < V / 4; ++i) {
-    const int c = (i * L + l) * 4;
-    float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-    if (live) {
+    for (int q = 0; q < V / C; ++q) {
+      const int c = (q * L + l) * C;
       if (vec) {
-        if (c < E) f = load4(row + c);
+        if (live && c < E) raw[q] = *reinterpret_cast<const uint4*>(row + c);
       } else {
-        if (c < E) f.x = to_f32(row[c]);
-        if (c + 1 < E) f.y = to_f32(row[c + 1]);
-        if (c + 2 < E) f.z = to_f32(row[c + 2]);
-        if (c + 3 < E) f.w = to_f32(row[c + 3]);
+        T v[C];
+#pragma unroll
+        for (int u = 0; u < C; ++u) v[u] = live && c + u < E ? row[c + u] : T(0.f);
+        raw[q] = *reinterpret_cast<const uint4*>(v);
       }
     }
-    v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
+  }
+  // values; -inf past the row's end, and throughout when it is not live
+  __device__ __forceinline__ void values(int E, int L, int l, bool live, float (&v)[V]) const {
+    constexpr int C = piece<T>();
+#pragma unroll
+    for (int q = 0; q < V / C; ++q) {
+      float f[C];
+      unpack(raw[q], f, T());
+#pragma unroll
+      for (int u = 0; u < C; ++u) v[q * C + u] = live && (q * L + l) * C + u < E ? f[u] : -INFINITY;
+    }
+  }
+};
+
+// N consecutive values from a lane's registers to memory
+template <typename OT, int N>
+__device__ __forceinline__ void store_run(OT* p, const float* v) {
+#pragma unroll
+  for (int b = 0; b < N; b += 16 / static_cast<int>(sizeof(OT))) {
+    constexpr int W = N < 16 / static_cast<int>(sizeof(OT)) ? N : 16 / static_cast<int>(sizeof(OT));
+    alignas(16) OT o[W];
+#pragma unroll
+    for (int u = 0; u < W; ++u) o[u] = from_f32(v[b + u], OT());
+    if constexpr (W * sizeof(OT) == 16)
+      *reinterpret_cast<uint4*>(p + b) = *reinterpret_cast<const uint4*>(o);
+    else
+      *reinterpret_cast<uint2*>(p + b) = *reinterpret_cast<const uint2*>(o);
   }
 }
 
@@ -108,6 +143,10 @@ __device__ __forceinline__ void softmax_row(float (&v)[V], int L) {
   const float inv = z == 0.f ? 0.f : __fdividef(1.f, z);
 #pragma unroll
   for (int i = 0; i < V; ++i) v[i] *= inv;
+}
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // First token at or after `t` belongs to the sequence this returns: the number
@@ -146,10 +185,7 @@ struct BalanceArgs {
 // First pass: block b sums the probabilities and counts of its chunk of
 // tokens, for each sequence in it.
 template <typename T, int V>
-__global__ void __launch_bounds__(kBalThreads) balance_partial_kernel(const BalanceArgs a) {
-  pdl_wait();
-  pdl_launch_dependents();
-  extern __shared__ float s_mem[];
+__device__ void balance_partial(const BalanceArgs& a, float* s_mem) {
   const int E = a.E, L = a.L;
   const int width = L * V;                                    // padded columns
   float* s_q = s_mem;                                          // [8 warps][width]
@@ -184,32 +220,35 @@ __global__ void __launch_bounds__(kBalThreads) balance_partial_kernel(const Bala
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
     // a warp's lanes run the same number of rounds: rows past the end are not live
-    constexpr int U = V <= 4 ? 4 : V <= 8 ? 2 : 1;  // rows loaded ahead of their use
-    for (int b = t; b < end; b += groups * U) {
-      float v[U][V];
+    auto counts_for = [&](int r) { return r < end && (!a.mask || a.mask[r]); };
+    Row<T, V> next;
+    bool next_live = counts_for(t + group);
+    next.load(logits + static_cast<size_t>(next_live ? t + group : t) * E, E, L, l, a.vec, next_live);
+    for (int b = t; b < end; b += groups) {
+      const Row<T, V> row = next;
+      const bool live = next_live;
+      const int r = b + groups + group;
+      next_live = counts_for(r);
+      next.load(logits + static_cast<size_t>(next_live ? r : t) * E, E, L, l, a.vec, next_live);
+      float v[V];
+      row.values(E, L, l, live, v);
+      softmax_row<V>(v, L);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int r = b + u * groups + group;
-        const bool live = r < end && (!a.mask || a.mask[r]);
-        load_row<T, V>(logits + static_cast<size_t>(live ? r : t) * E, E, L, l, a.vec, live, v[u]);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        softmax_row<V>(v[u], L);
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] += v[u][i];
-      }
+      for (int i = 0; i < V; ++i) acc[i] += v[i];
     }
     int n = 0;
-    for (int r = t + tid; r < end; r += kBalThreads) n += !a.mask || a.mask[r];
-    const long long p1 = static_cast<long long>(end) * a.k;
-    for (long long p = static_cast<long long>(t) * a.k + tid; p < p1; p += kBalThreads) {
-      if (a.mask && !a.mask[p / a.k]) continue;
-      const int e = a.idx[p];
-      if (e >= 0 && e < E)
-        atomicAdd(&s_c[e], 1);   // whole numbers: the order does not show
-      else if (e != -1)
-        atomicOr(&s_err, 1);
+    for (int r = t + tid; r < end; r += kBalThreads) {
+      if (!counts_for(r)) continue;
+      ++n;
+      const int32_t* ids = a.idx + static_cast<size_t>(r) * a.k;
+#pragma unroll 4
+      for (int j = 0; j < a.k; ++j) {
+        const int e = ids[j];
+        if (e >= 0 && e < E)
+          atomicAdd(&s_c[e], 1);   // whole numbers: the order does not show
+        else if (e != -1)
+          atomicOr(&s_err, 1);
+      }
     }
     // the warp's rows, then the block's warps, in a fixed order
 #pragma unroll
@@ -217,9 +256,9 @@ __global__ void __launch_bounds__(kBalThreads) balance_partial_kernel(const Bala
       for (int o = L; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
     if (lane < L) {
 #pragma unroll
-      for (int i = 0; i < V / 4; ++i)
-        *reinterpret_cast<float4*>(s_q + warp * width + (i * L + l) * 4) =
-            make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+      for (int i = 0; i < V; i += 4)
+        *reinterpret_cast<float4*>(s_q + warp * width + column<T>(i, L, l)) =
+            make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
     }
     __shared__ int s_n[kBalThreads / 32];
     n = __reduce_add_sync(0xffffffffu, n);
@@ -247,20 +286,16 @@ __global__ void __launch_bounds__(kBalThreads) balance_partial_kernel(const Bala
 // Second pass, one cluster: CTA r reduces its slice of the experts over the
 // slots of every sequence, `w` threads to a column and `g` sequences at once;
 // the CTAs' shares of the loss meet in rank order.
-__global__ void __launch_bounds__(kFinThreads) __cluster_dims__(kFinCluster, 1, 1)
-    balance_finish_kernel(const BalanceArgs a, int cols, int w) {
-  pdl_wait();
-  pdl_launch_dependents();
-  __shared__ float s_q[kFinThreads];
-  __shared__ int s_c[kFinThreads];
-  __shared__ int s_tok[kFinThreads];
+template <int NT>
+__device__ void balance_finish(const BalanceArgs& a, int cols, int w) {
+  __shared__ float s_q[NT];
+  __shared__ int s_c[NT];
+  __shared__ int s_tok[NT];
   __shared__ float s_loss[kFinCluster];
   __shared__ int s_live;
   const int tid = threadIdx.x;
   uint32_t rank;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  // every CTA of the cluster runs before another one writes to its shared memory (waited for below)
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int E = a.E;
   auto slots = [&](int s, int& first, int& last) {  // [first, last) of sequence s
     const int b = a.off ? max(0, min(a.T, a.off[s])) : 0, e = a.off ? max(0, min(a.T, a.off[s + 1])) : a.T;
@@ -269,7 +304,7 @@ __global__ void __launch_bounds__(kFinThreads) __cluster_dims__(kFinCluster, 1, 
   };
   // sequences that have tokens
   int live = 0;
-  for (int s0 = 0; s0 < a.S; s0 += kFinThreads) {
+  for (int s0 = 0; s0 < a.S; s0 += NT) {
     bool some = false;
     if (s0 + tid < a.S) {
       int f, e;
@@ -279,7 +314,7 @@ __global__ void __launch_bounds__(kFinThreads) __cluster_dims__(kFinCluster, 1, 
     live += __syncthreads_count(some);
   }
   if (tid == 0) s_live = live;
-  const int g = kFinThreads / (cols * w);                   // sequences at once
+  const int g = NT / (cols * w);                   // sequences at once
   const int col = tid % cols, j = tid / cols % w, sg = tid / (cols * w);
   const int e = rank * cols + col;
   float share = 0.f;
@@ -290,7 +325,7 @@ __global__ void __launch_bounds__(kFinThreads) __cluster_dims__(kFinCluster, 1, 
     if (s < a.S && e < E) {
       int f, l;
       slots(s, f, l);
-#pragma unroll 4
+#pragma unroll 8
       for (int i = f + j; i < l; i += w) {
         q += a.part_q[static_cast<size_t>(i) * E + e];
         c += a.part_c[static_cast<size_t>(i) * E + e];
@@ -320,20 +355,19 @@ __global__ void __launch_bounds__(kFinThreads) __cluster_dims__(kFinCluster, 1, 
   }
   // the block's share, summed in thread order by halves
   s_q[tid] = share;
-  for (int o = kFinThreads >> 1; o; o >>= 1) {
+  for (int o = NT >> 1; o; o >>= 1) {
     __syncthreads();
     if (tid < o) s_q[tid] += s_q[tid + o];
   }
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   if (tid == 0) {
     uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(&s_loss[rank])), there;
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(there) : "r"(at));
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(s_q[0]) : "memory");
   }
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_barrier();
   if (rank == 0) {
     int err = 0;
-    for (int i = tid; i < a.chunks; i += kFinThreads) err |= a.part_err[i];
+    for (int i = tid; i < a.chunks; i += NT) err |= a.part_err[i];
     const int bad = __syncthreads_or(err & 2), odd = __syncthreads_or(err & 1);
     if (tid == 0) {
       float all = 0.f;
@@ -342,6 +376,35 @@ __global__ void __launch_bounds__(kFinThreads) __cluster_dims__(kFinCluster, 1, 
       *a.status = bad ? MOE_ERR_BAD_OFFSETS : odd ? MOE_ERR_INVALID : MOE_OK;
     }
   }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kBalThreads) balance_partial_kernel(const BalanceArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  extern __shared__ float s_mem[];
+  balance_partial<T, V>(a, s_mem);
+}
+
+__global__ void __launch_bounds__(kFinThreads) __cluster_dims__(kFinCluster, 1, 1)
+    balance_finish_kernel(const BalanceArgs a, int cols, int w) {
+  pdl_wait();
+  pdl_launch_dependents();
+  // every CTA of the cluster runs before another one writes to its shared memory
+  cluster_barrier();
+  balance_finish<kFinThreads>(a, cols, w);
+}
+
+// Both passes of a small batch in one launch, the cluster's CTAs a chunk each.
+template <typename T, int V>
+__global__ void __launch_bounds__(kBalThreads) __cluster_dims__(kFinCluster, 1, 1)
+    balance_small_kernel(const BalanceArgs a, int cols, int w) {
+  pdl_wait();
+  pdl_launch_dependents();
+  extern __shared__ float s_mem[];
+  if (static_cast<int>(blockIdx.x) < a.chunks) balance_partial<T, V>(a, s_mem);
+  cluster_barrier();   // the partial sums are there, in global memory
+  balance_finish<kBalThreads>(a, cols, w);
 }
 
 struct RouterGradArgs {
@@ -359,107 +422,140 @@ struct RouterGradArgs {
   int chunk, L, vec;
 };
 
-template <typename T, typename OT, int V>
-__global__ void __launch_bounds__(kBalThreads) router_backward_kernel(const RouterGradArgs a) {
+template <typename T, typename OT, int V, bool kRenorm>
+__global__ void __launch_bounds__(kBalThreads, V <= 8 ? 3 : 1) router_backward_kernel(const RouterGradArgs a) {
   pdl_wait();
   pdl_launch_dependents();
+  constexpr int KB = 4;   // slots held at once
   const int E = a.E, L = a.L;
   const int tid = threadIdx.x, lane = tid & 31;
   const int l = lane % L, group = tid / L, groups = kBalThreads / L;
   const T* logits = static_cast<const T*>(a.logits);
   OT* out = static_cast<OT*>(a.out);
   const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
+  // one renormalised gate is 1 whatever its logit
+  const bool gates = a.d_w && !(kRenorm && a.k == 1);
   int s = a.counts && a.off ? sequence_at(a.off, a.S, t0) : 0;
   int held = -1;        // the sequence whose counts are in bal
   float bal[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) bal[i] = 0.f;
   const float d_loss = a.counts && a.d_loss ? __ldg(a.d_loss) : 1.f;
+
+  struct Slots {
+    int e[KB];
+    float g[KB];
+  };
+  auto load_slots = [&](int t, int j0, Slots& z) {
+    const int32_t* ids = a.idx + static_cast<size_t>(t) * a.k + j0;
+    const float* g = a.d_w + static_cast<size_t>(t) * a.k + j0;
+#pragma unroll
+    for (int j = 0; j < KB; ++j) {
+      z.e[j] = j0 + j < a.k ? __ldg(ids + j) : -1;
+      z.g[j] = j0 + j < a.k ? __ldg(g + j) : 0.f;
+    }
+  };
+  Row<T, V> next;
+  Slots next_slots;
+  auto prefetch = [&](int t) {
+    const bool live = t < t1;
+    next.load(logits + static_cast<size_t>(live ? t : t0) * E, E, L, l, a.vec, live);
+    if (gates) load_slots(live ? t : t0, 0, next_slots);
+  };
+  prefetch(t0 + group);
   for (int b = t0; b < t1; b += groups) {
     const int t = b + group;
     const bool live = t < t1;
     const int tr = live ? t : t0;
-    float p[V], G[V];
-    load_row<T, V>(logits + static_cast<size_t>(tr) * E, E, L, l, a.vec, live, p);
+    float p[V], G[V], n[V];   // n: how many of the slots chose the column
+    next.values(E, L, l, live, p);
+    Slots slots = next_slots;
+    if (b + groups < t1) prefetch(t + groups);
     bool any = false;   // something to differentiate: else the row's gradient is 0 whatever its logits hold
 #pragma unroll
-    for (int i = 0; i < V; ++i) G[i] = 0.f;
+    for (int i = 0; i < V; ++i) G[i] = n[i] = 0.f;
+    if (gates) {
+      for (int j0 = 0; j0 < a.k; j0 += KB) {
+        if (j0) load_slots(tr, j0, slots);
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+          if (j0 + j >= a.k) break;
+          any |= slots.g[j] != 0.f;
+          const int at = slots.e[j] - l * piece<T>();   // the column as seen from this lane's first
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const bool mine = at == i / piece<T>() * L * piece<T>() + i % piece<T>();
+            G[i] += mine ? slots.g[j] : 0.f;
+            if (kRenorm) n[i] += mine ? 1.f : 0.f;
+          }
+        }
+      }
+    }
+    softmax_row<V>(p, L);
+    if (gates && kRenorm) {
+      // over the selected experts alone: w = p / z, their gradient w (g - sum w g)
+      float z = 0.f, wg = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        z = fmaf(p[i], n[i], z);
+        wg = fmaf(p[i], G[i], wg);
+      }
+      z = group_sum(z, L);
+      wg = group_sum(wg, L);
+      const float inv = z == 0.f ? 0.f : __fdiv_rn(1.f, z);
+      wg *= inv;
+#pragma unroll
+      for (int i = 0; i < V; ++i) G[i] = p[i] * inv * (G[i] - n[i] * wg);
+    }
     if (a.counts) {
       while (a.off && s < a.S && a.off[s + 1] <= tr) ++s;
       const bool in = s < a.S && (!a.mask || a.mask[tr]);
       if (in && held != s) {
         held = s;
         const float c = __ldg(a.coef + s) * d_loss;
-        const int32_t* n = a.counts + static_cast<size_t>(s) * E;
+        const int32_t* cnt = a.counts + static_cast<size_t>(s) * E;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const int e = ((i >> 2) * L + l) * 4 + (i & 3);
-          bal[i] = e < E ? c * static_cast<float>(__ldg(n + e)) : 0.f;
+          const int e = column<T>(i, L, l);
+          bal[i] = e < E ? c * static_cast<float>(__ldg(cnt + e)) : 0.f;
         }
       }
-      any = in;
-      if (in) {
+      any |= in;
+      if (gates && kRenorm) {   // p (b - sum b p) beside the gates' gradient
+        float dot = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) G[i] = bal[i];
+        for (int i = 0; i < V; ++i) dot = fmaf(p[i], in ? bal[i] : 0.f, dot);
+        dot = group_sum(dot, L);
+#pragma unroll
+        for (int i = 0; i < V; ++i) G[i] = fmaf(p[i], (in ? bal[i] : 0.f) - dot, G[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) G[i] += in ? bal[i] : 0.f;
       }
     }
-    const int32_t* idx = a.idx + static_cast<size_t>(tr) * a.k;
-    const float* d_w = a.d_w ? a.d_w + static_cast<size_t>(tr) * a.k : nullptr;
-    if (d_w && !a.renorm) {
-      for (int j = 0; j < a.k; ++j) {
-        const int e = __ldg(idx + j);
-        const float g = __ldg(d_w + j);
-        any |= g != 0.f;
+    if (!(gates && kRenorm)) {
+      float dot = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) G[i] += ((i >> 2) * L + l) * 4 + (i & 3) == e ? g : 0.f;
-      }
-    }
-    softmax_row<V>(p, L);
-    float dot = 0.f;
+      for (int i = 0; i < V; ++i) dot = fmaf(p[i], G[i], dot);
+      dot = group_sum(dot, L);
 #pragma unroll
-    for (int i = 0; i < V; ++i) dot = fmaf(p[i], G[i], dot);
-    dot = group_sum(dot, L);
-#pragma unroll
-    for (int i = 0; i < V; ++i) G[i] = p[i] * (G[i] - dot);
-    if (d_w && a.renorm) {  // over the selected experts: w = p / sum, one expert's weight is exactly 1
-      float z = 0.f;
-      for (int j = 0; j < a.k; ++j) {
-        const int e = __ldg(idx + j);
-        any |= __ldg(d_w + j) != 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) z += ((i >> 2) * L + l) * 4 + (i & 3) == e ? p[i] : 0.f;
-      }
-      z = group_sum(z, L);
-      const float zs = z == 0.f ? 1.f : z;
-      float wd = 0.f;
-      for (int j = 0; j < a.k; ++j) {
-        const int e = __ldg(idx + j);
-        const float g = __ldg(d_w + j);
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          wd += ((i >> 2) * L + l) * 4 + (i & 3) == e ? __fdiv_rn(p[i], zs) * g : 0.f;
-      }
-      wd = group_sum(wd, L);
-      for (int j = 0; j < a.k; ++j) {
-        const int e = __ldg(idx + j);
-        const float g = __ldg(d_w + j);
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (((i >> 2) * L + l) * 4 + (i & 3) == e) G[i] += __fdiv_rn(p[i], zs) * (g - wd);
-      }
+      for (int i = 0; i < V; ++i) G[i] = p[i] * (G[i] - dot);
     }
     if (!live) continue;
     OT* row = out + static_cast<size_t>(t) * E;
 #pragma unroll
-    for (int i = 0; i < V / 4; ++i) {
-      const int c = (i * L + l) * 4;
-      if (!any) G[4 * i] = G[4 * i + 1] = G[4 * i + 2] = G[4 * i + 3] = 0.f;
+    for (int q = 0; q < V / piece<T>(); ++q) {
+      constexpr int C = piece<T>();
+      const int c = (q * L + l) * C;
+      float v[C];
+#pragma unroll
+      for (int u = 0; u < C; ++u) v[u] = any ? G[q * C + u] : 0.f;
       if (a.vec) {
-        if (c < E) store4(row + c, make_float4(G[4 * i], G[4 * i + 1], G[4 * i + 2], G[4 * i + 3]));
+        if (c < E) store_run<OT, C>(row + c, v);
       } else {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (c + u < E) row[c + u] = from_f32(G[4 * i + u], OT());
+        for (int u = 0; u < C; ++u)
+          if (c + u < E) row[c + u] = from_f32(v[u], OT());
       }
     }
   }
@@ -470,34 +566,35 @@ int lanes_for(int E, int V) {  // lanes of a row: a power of two, V columns each
   while (L < 32 && L * V < E) L *= 2;
   return L;
 }
-int values_for(int E) { return E <= 128 ? 4 : E <= 256 ? 8 : E <= 512 ? 16 : 32; }
+int values_for(int E) { return E <= 256 ? 8 : 32; }
 
 int balance_chunk(int T) {
+  if (T <= kBalSmall) return T > 0 ? (T + kFinCluster - 1) / kFinCluster : 1;
   const int c = (T + kBalMaxChunks - 1) / kBalMaxChunks;
   return c < kBalMinChunk ? kBalMinChunk : c;
 }
 
 template <typename T>
-int launch_partial(const BalanceArgs& a, int V, cudaStream_t s) {
+int launch_partial(const BalanceArgs& a, int V, int cols, int w, cudaStream_t s) {
   const size_t smem = (static_cast<size_t>(kBalThreads / 32) * a.L * V + a.E) * 4;
   const dim3 grid(a.chunks), block(kBalThreads);
-  switch (V) {
-    case 4: return launch_pdl(__func__, balance_partial_kernel<T, 4>, grid, block, smem, s, a);
-    case 8: return launch_pdl(__func__, balance_partial_kernel<T, 8>, grid, block, smem, s, a);
-    case 16: return launch_pdl(__func__, balance_partial_kernel<T, 16>, grid, block, smem, s, a);
-    default: return launch_pdl(__func__, balance_partial_kernel<T, 32>, grid, block, smem, s, a);
+  if (a.T <= kBalSmall) {
+    const dim3 one(kFinCluster);
+    if (V == 8) return launch_pdl(__func__, balance_small_kernel<T, 8>, one, block, smem, s, a, cols, w);
+    return launch_pdl(__func__, balance_small_kernel<T, 32>, one, block, smem, s, a, cols, w);
   }
+  if (V == 8) return launch_pdl(__func__, balance_partial_kernel<T, 8>, grid, block, smem, s, a);
+  return launch_pdl(__func__, balance_partial_kernel<T, 32>, grid, block, smem, s, a);
 }
 
 template <typename T, typename OT>
 int launch_grad(const RouterGradArgs& a, int V, int grid, cudaStream_t s) {
   const dim3 g(grid), b(kBalThreads);
-  switch (V) {
-    case 4: return launch_pdl(__func__, router_backward_kernel<T, OT, 4>, g, b, 0, s, a);
-    case 8: return launch_pdl(__func__, router_backward_kernel<T, OT, 8>, g, b, 0, s, a);
-    case 16: return launch_pdl(__func__, router_backward_kernel<T, OT, 16>, g, b, 0, s, a);
-    default: return launch_pdl(__func__, router_backward_kernel<T, OT, 32>, g, b, 0, s, a);
-  }
+  if (V == 8)
+    return a.renorm ? launch_pdl(__func__, router_backward_kernel<T, OT, 8, true>, g, b, 0, s, a)
+                    : launch_pdl(__func__, router_backward_kernel<T, OT, 8, false>, g, b, 0, s, a);
+  return a.renorm ? launch_pdl(__func__, router_backward_kernel<T, OT, 32, true>, g, b, 0, s, a)
+                  : launch_pdl(__func__, router_backward_kernel<T, OT, 32, false>, g, b, 0, s, a);
 }
 
 template <typename T>
@@ -524,7 +621,7 @@ int launch_balance_loss(const void* logits, int dtype, const int32_t* idx, int T
   a.chunk = balance_chunk(T);
   a.chunks = T > 0 ? (T + a.chunk - 1) / a.chunk : 0;
   a.L = lanes_for(E, V);
-  a.vec = E % 4 == 0;
+  a.vec = E % (dtype == MOE_F32 ? 4 : 8) == 0;
   const size_t slots = static_cast<size_t>(a.chunks) + S, m = align_up(slots * E * 4, 256);
   char* p = static_cast<char*>(ws);
   a.status = reinterpret_cast<int*>(p);
@@ -533,18 +630,17 @@ int launch_balance_loss(const void* logits, int dtype, const int32_t* idx, int T
   a.part_n = reinterpret_cast<int32_t*>(p + 256 + 2 * m);
   a.part_err = reinterpret_cast<int32_t*>(p + 256 + 2 * m + align_up(slots * 4, 256));
   a.loss = loss, a.counts = counts, a.prob = prob, a.coef = coef;
-  if (a.chunks) {
-    const int st = dtype == MOE_F32   ? launch_partial<float>(a, V, s)
-                   : dtype == MOE_F16 ? launch_partial<__half>(a, V, s)
-                                      : launch_partial<__nv_bfloat16>(a, V, s);
-    if (st != MOE_OK) return st;
-  }
-  // columns of a CTA and threads of a column, powers of two: as many threads
-  // as a sequence has slots, on average
+  // columns of a CTA and threads of a column, powers of two: a thread sums
+  // eight slots of a sequence, on average, with their loads in flight together
+  const int threads = T <= kBalSmall ? kBalThreads : kFinThreads;
   int cols = 8;
   while (cols * kFinCluster < E) cols *= 2;
   int w = 1;
-  while (w * cols < kFinThreads && w < a.chunks / (S > 0 ? S : 1) + 1) w *= 2;
+  while (w * cols < threads && w * 8 < a.chunks / S + 1) w *= 2;
+  const int st = dtype == MOE_F32   ? launch_partial<float>(a, V, cols, w, s)
+                 : dtype == MOE_F16 ? launch_partial<__half>(a, V, cols, w, s)
+                                    : launch_partial<__nv_bfloat16>(a, V, cols, w, s);
+  if (st != MOE_OK || T <= kBalSmall) return st;
   return launch_pdl(__func__, balance_finish_kernel, dim3(kFinCluster), dim3(kFinThreads), 0, s, a, cols, w);
 }
 
@@ -557,9 +653,9 @@ int launch_router_backward(const void* logits, int dtype, const int32_t* idx, co
   a.logits = logits, a.idx = idx, a.d_w = d_w, a.T = T, a.E = E, a.k = k, a.renorm = renorm, a.off = off, a.S = S;
   a.mask = mask, a.counts = counts, a.coef = coef, a.d_loss = d_loss, a.out = out;
   a.L = lanes_for(E, V);
-  a.vec = E % 4 == 0;
+  a.vec = E % (dtype == MOE_F32 ? 4 : 8) == 0;   // then rows of every output type are stored whole too
   const int groups = kBalThreads / a.L;
-  const int blocks = num_sms() * 8;
+  const int blocks = num_sms() * 3;   // one wave
   a.chunk = (T + blocks - 1) / blocks;
   a.chunk = (a.chunk + groups - 1) / groups * groups;
   const int grid = (T + a.chunk - 1) / a.chunk;

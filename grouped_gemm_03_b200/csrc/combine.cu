@@ -209,8 +209,10 @@ template <typename GT>
 int launch_combine_grad(const GT* dout, const __nv_bfloat16* y, const int32_t* t2r, const float* w, int has_shared,
                         int T, int d, int k, const int32_t* shared_base, __nv_bfloat16* dy, float* dw,
                         cudaStream_t s) {
-  // a thread's share is one or more 16-byte pieces; narrow rows take fewer threads
-  const dim3 grid(T), block(d <= 256 ? 32 : d <= 1024 ? 128 : 256);
+  // threads that share a row's 16-byte pieces evenly: 7168 columns are 4 rounds
+  // of 224 threads, where 256 threads would sit half idle in the fourth
+  const int pieces = d / 8, rounds = (pieces + 255) / 256, per = (pieces + rounds - 1) / rounds;
+  const dim3 grid(T), block((per + 31) / 32 * 32);
   const char* where = "combine_backward_kernel";
   if (k == 1)
     return launch_pdl(where, combine_backward_kernel<GT, 1>, grid, block, 0, s, dout, y, t2r, w, has_shared, T, d, k,
