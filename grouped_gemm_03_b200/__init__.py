@@ -418,13 +418,11 @@ def balance_loss(logits, topk_idx, alpha: float, seq_offsets=None, mask=None, wa
     L = lib()
     ws = _workspace(logits, ws, L.moe_balance_loss_workspace_size(T, E, S))
     counts = topk_idx.new_empty((S, E))
-    # loss and coef share an allocation: the one is a row before the other's
-    both = logits.new_empty(S + 1, dtype=torch.float32)
-    loss, coef = both.split((1, S))
+    loss = logits.new_empty(1, dtype=torch.float32)
+    coef = logits.new_empty(S, dtype=torch.float32)
     prob = logits.new_empty((S, E), dtype=torch.float32) if want_prob else None
-    p_both = both.data_ptr()
-    st = L.moe_balance_loss(p_l, _TORCH_DT[logits.dtype], p_i, T, E, k, p_o, S, p_m, alpha, p_both, counts.data_ptr(),
-                            prob.data_ptr() if want_prob else None, p_both + 4, ws.data_ptr(), ws.numel(),
+    st = L.moe_balance_loss(p_l, _TORCH_DT[logits.dtype], p_i, T, E, k, p_o, S, p_m, alpha, loss.data_ptr(),
+                            counts.data_ptr(), prob.data_ptr() if want_prob else None, coef.data_ptr(), ws.data_ptr(), ws.numel(),
                             _stream_of(dev))
     _check(st, "moe_balance_loss")
     return loss, counts, prob, coef

@@ -17,7 +17,7 @@
 //   w_j = p_j / sum_S p,   dlogit_{idx_j} += w_j (dw_j - sum_S w dw).
 //
 // Both kernels are bound by reading the logits (and writing their gradient):
-// one pass, each row held in registers by L lanes of 8 columns (32 past 256
+// one pass, each row held in registers by L lanes of 16 columns (32 past 512
 // experts), the softmax's maximum and sum by shuffles.
 #include "common.cuh"
 
@@ -63,36 +63,44 @@ __device__ __forceinline__ float from_f32(float v, float) { return v; }
 __device__ __forceinline__ __half from_f32(float v, __half) { return __float2half_rn(v); }
 __device__ __forceinline__ __nv_bfloat16 from_f32(float v, __nv_bfloat16) { return __float2bfloat16_rn(v); }
 
+__device__ __forceinline__ uint32_t minus_inf_bits(float) { return 0xff800000u; }
+__device__ __forceinline__ uint32_t minus_inf_bits(__half) { return 0xfc00fc00u; }
+__device__ __forceinline__ uint32_t minus_inf_bits(__nv_bfloat16) { return 0xff80ff80u; }
+
 // A lane's share of a row as it lies in memory, so that the next rows' loads
 // can be in flight while this one is worked on.  vec: every row starts on 16
 // bytes and E fills whole pieces.
 template <typename T, int V>
 struct Row {
   uint4 raw[V / piece<T>()];
+  // -inf past the row's end, and throughout when it is not live
   __device__ __forceinline__ void load(const T* row, int E, int L, int l, bool vec, bool live) {
     constexpr int C = piece<T>();
+    const uint32_t none = minus_inf_bits(T());
 #pragma unroll
     for (int q = 0; q < V / C; ++q) {
       const int c = (q * L + l) * C;
+      raw[q] = make_uint4(none, none, none, none);
       if (vec) {
         if (live && c < E) raw[q] = *reinterpret_cast<const uint4*>(row + c);
-      } else {
-        T v[C];
+      } else if (live) {
+        alignas(16) T v[C];
+        *reinterpret_cast<uint4*>(v) = raw[q];
 #pragma unroll
-        for (int u = 0; u < C; ++u) v[u] = live && c + u < E ? row[c + u] : T(0.f);
+        for (int u = 0; u < C; ++u)
+          if (c + u < E) v[u] = row[c + u];
         raw[q] = *reinterpret_cast<const uint4*>(v);
       }
     }
   }
-  // values; -inf past the row's end, and throughout when it is not live
-  __device__ __forceinline__ void values(int E, int L, int l, bool live, float (&v)[V]) const {
+  __device__ __forceinline__ void values(float (&v)[V]) const {
     constexpr int C = piece<T>();
 #pragma unroll
     for (int q = 0; q < V / C; ++q) {
       float f[C];
       unpack(raw[q], f, T());
 #pragma unroll
-      for (int u = 0; u < C; ++u) v[q * C + u] = live && (q * L + l) * C + u < E ? f[u] : -INFINITY;
+      for (int u = 0; u < C; ++u) v[q * C + u] = f[u];
     }
   }
 };
@@ -122,13 +130,14 @@ __device__ __forceinline__ float group_sum(float v, int L) {
   return v;
 }
 
-// Softmax of a row in place.  A logit of -inf has probability 0; a row of
-// nothing else (a row that is not live is one) has probability 0 throughout.
-// The maximum passes over a NaN, the sum does not, so a NaN logit makes its
-// row NaN.
+// The numerators e^(v - m) of a row's softmax in place of its values, with the
+// row's maximum m and 1 / (their sum).  A logit of -inf has probability 0; a
+// row of nothing else (a row that is not live is one) has probability 0
+// throughout: inv = 0.  The maximum passes over a NaN, the sum does not, so a
+// NaN logit makes its row NaN.
 template <int V>
-__device__ __forceinline__ void softmax_row(float (&v)[V], int L) {
-  float m = v[0];
+__device__ __forceinline__ void softmax_row(float (&v)[V], int L, float& m, float& inv) {
+  m = v[0];
 #pragma unroll
   for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
   m = group_max(m, L);
@@ -140,9 +149,7 @@ __device__ __forceinline__ void softmax_row(float (&v)[V], int L) {
     z += v[i];
   }
   z = group_sum(z, L);
-  const float inv = z == 0.f ? 0.f : __fdividef(1.f, z);
-#pragma unroll
-  for (int i = 0; i < V; ++i) v[i] *= inv;
+  inv = z == 0.f ? 0.f : __fdividef(1.f, z);
 }
 
 __device__ __forceinline__ void cluster_barrier() {
@@ -226,15 +233,14 @@ __device__ void balance_partial(const BalanceArgs& a, float* s_mem) {
     next.load(logits + static_cast<size_t>(next_live ? t + group : t) * E, E, L, l, a.vec, next_live);
     for (int b = t; b < end; b += groups) {
       const Row<T, V> row = next;
-      const bool live = next_live;
       const int r = b + groups + group;
       next_live = counts_for(r);
       next.load(logits + static_cast<size_t>(next_live ? r : t) * E, E, L, l, a.vec, next_live);
-      float v[V];
-      row.values(E, L, l, live, v);
-      softmax_row<V>(v, L);
+      float v[V], m, inv;
+      row.values(v);
+      softmax_row<V>(v, L, m, inv);
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += v[i];
+      for (int i = 0; i < V; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
     }
     int n = 0;
     for (int r = t + tid; r < end; r += kBalThreads) {
@@ -288,11 +294,8 @@ __device__ void balance_partial(const BalanceArgs& a, float* s_mem) {
 // the CTAs' shares of the loss meet in rank order.
 template <int NT>
 __device__ void balance_finish(const BalanceArgs& a, int cols, int w) {
-  __shared__ float s_q[NT];
-  __shared__ int s_c[NT];
-  __shared__ int s_tok[NT];
+  __shared__ float s_warp[NT / 32];
   __shared__ float s_loss[kFinCluster];
-  __shared__ int s_live;
   const int tid = threadIdx.x;
   uint32_t rank;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -313,16 +316,17 @@ __device__ void balance_finish(const BalanceArgs& a, int cols, int w) {
     }
     live += __syncthreads_count(some);
   }
-  if (tid == 0) s_live = live;
-  const int g = NT / (cols * w);                   // sequences at once
-  const int col = tid % cols, j = tid / cols % w, sg = tid / (cols * w);
+  // the w lanes of a (sequence, column) are neighbours: their sums meet by shuffles
+  const int g = NT / (cols * w);                            // sequences at once
+  const int j = tid % w, col = tid / w % cols, sg = tid / (cols * w);
   const int e = rank * cols + col;
   float share = 0.f;
   for (int s0 = 0; s0 < a.S; s0 += g) {
     const int s = s0 + sg;
+    const bool in = s < a.S && e < E;
     float q = 0.f;
     int c = 0, n = 0;
-    if (s < a.S && e < E) {
+    if (in) {
       int f, l;
       slots(s, f, l);
 #pragma unroll 8
@@ -332,37 +336,31 @@ __device__ void balance_finish(const BalanceArgs& a, int cols, int w) {
         n += a.part_n[i];
       }
     }
-    s_q[tid] = q, s_c[tid] = c, s_tok[tid] = n;
     for (int o = w >> 1; o; o >>= 1) {
-      __syncthreads();
-      if (j < o) {
-        s_q[tid] += s_q[tid + o * cols];
-        s_c[tid] += s_c[tid + o * cols];
-        s_tok[tid] += s_tok[tid + o * cols];
-      }
+      q += __shfl_xor_sync(0xffffffffu, q, o);
+      c += __shfl_xor_sync(0xffffffffu, c, o);
+      n += __shfl_xor_sync(0xffffffffu, n, o);
     }
-    __syncthreads();
-    if (j == 0 && s < a.S && e < E) {
-      q = s_q[tid], c = s_c[tid], n = s_tok[tid];
+    if (j == 0 && in) {
       const float nf = static_cast<float>(n);
-      const float k_s = n > 0 ? __fdiv_rn(a.alpha * E, a.k * nf * nf * static_cast<float>(s_live)) : 0.f;
+      const float k_s = n > 0 ? __fdiv_rn(a.alpha * E, a.k * nf * nf * static_cast<float>(live)) : 0.f;
       a.counts[static_cast<size_t>(s) * E + e] = c;
       if (a.prob) a.prob[static_cast<size_t>(s) * E + e] = n > 0 ? __fdiv_rn(q, nf) : 0.f;
       if (e == 0) a.coef[s] = k_s;
       share += k_s * (static_cast<float>(c) * q);
     }
-    __syncthreads();
   }
-  // the block's share, summed in thread order by halves
-  s_q[tid] = share;
-  for (int o = NT >> 1; o; o >>= 1) {
-    __syncthreads();
-    if (tid < o) s_q[tid] += s_q[tid + o];
-  }
+  // the block's share of the loss, in a fixed order
+#pragma unroll
+  for (int o = 16; o; o >>= 1) share += __shfl_xor_sync(0xffffffffu, share, o);
+  if ((tid & 31) == 0) s_warp[tid >> 5] = share;
+  __syncthreads();
   if (tid == 0) {
+    float all = 0.f;
+    for (int i = 0; i < NT / 32; ++i) all += s_warp[i];
     uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(&s_loss[rank])), there;
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(there) : "r"(at));
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(s_q[0]) : "memory");
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(all) : "memory");
   }
   cluster_barrier();
   if (rank == 0) {
@@ -422,140 +420,147 @@ struct RouterGradArgs {
   int chunk, L, vec;
 };
 
+// The dense part of a row, p (bal - dot), is written in whole pieces; the
+// selected experts' entries are then written over it by the lanes that hold
+// the slots (lane l slots l and l + L), which read their own logit again: a
+// search of the row's registers for k columns would cost more than the softmax.
 template <typename T, typename OT, int V, bool kRenorm>
-__global__ void __launch_bounds__(kBalThreads, V <= 8 ? 3 : 1) router_backward_kernel(const RouterGradArgs a) {
+__global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 1) router_backward_kernel(const RouterGradArgs a) {
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int KB = 4;   // slots held at once
-  const int E = a.E, L = a.L;
+  const int E = a.E, L = a.L, k = a.k;
   const int tid = threadIdx.x, lane = tid & 31;
   const int l = lane % L, group = tid / L, groups = kBalThreads / L;
   const T* logits = static_cast<const T*>(a.logits);
   OT* out = static_cast<OT*>(a.out);
   const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
   // one renormalised gate is 1 whatever its logit
-  const bool gates = a.d_w && !(kRenorm && a.k == 1);
+  const bool gates = a.d_w && !(kRenorm && k == 1);
   int s = a.counts && a.off ? sequence_at(a.off, a.S, t0) : 0;
   int held = -1;        // the sequence whose counts are in bal
+  float c_s = 0.f;
   float bal[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) bal[i] = 0.f;
   const float d_loss = a.counts && a.d_loss ? __ldg(a.d_loss) : 1.f;
 
-  struct Slots {
-    int e[KB];
-    float g[KB];
-  };
-  auto load_slots = [&](int t, int j0, Slots& z) {
-    const int32_t* ids = a.idx + static_cast<size_t>(t) * a.k + j0;
-    const float* g = a.d_w + static_cast<size_t>(t) * a.k + j0;
-#pragma unroll
-    for (int j = 0; j < KB; ++j) {
-      z.e[j] = j0 + j < a.k ? __ldg(ids + j) : -1;
-      z.g[j] = j0 + j < a.k ? __ldg(g + j) : 0.f;
-    }
-  };
   Row<T, V> next;
-  Slots next_slots;
+  int next_e[2] = {-1, -1};
+  float next_g[2] = {0.f, 0.f};
   auto prefetch = [&](int t) {
     const bool live = t < t1;
-    next.load(logits + static_cast<size_t>(live ? t : t0) * E, E, L, l, a.vec, live);
-    if (gates) load_slots(live ? t : t0, 0, next_slots);
+    const size_t tr = live ? t : t0;
+    next.load(logits + tr * E, E, L, l, a.vec, live);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const bool in = gates && live && l + u * L < k;
+      next_e[u] = in ? __ldg(a.idx + tr * k + l + u * L) : -1;
+      next_g[u] = in ? __ldg(a.d_w + tr * k + l + u * L) : 0.f;
+    }
   };
   prefetch(t0 + group);
   for (int b = t0; b < t1; b += groups) {
     const int t = b + group;
     const bool live = t < t1;
     const int tr = live ? t : t0;
-    float p[V], G[V], n[V];   // n: how many of the slots chose the column
-    next.values(E, L, l, live, p);
-    Slots slots = next_slots;
+    const T* row = logits + static_cast<size_t>(tr) * E;
+    float p[V], m, inv;
+    next.values(p);
+    int e[2];
+    float g[2], x[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      e[u] = next_e[u] >= 0 && next_e[u] < E ? next_e[u] : -1;
+      g[u] = next_g[u];
+      x[u] = e[u] >= 0 ? to_f32(row[e[u]]) : -INFINITY;
+    }
     if (b + groups < t1) prefetch(t + groups);
-    bool any = false;   // something to differentiate: else the row's gradient is 0 whatever its logits hold
-#pragma unroll
-    for (int i = 0; i < V; ++i) G[i] = n[i] = 0.f;
-    if (gates) {
-      for (int j0 = 0; j0 < a.k; j0 += KB) {
-        if (j0) load_slots(tr, j0, slots);
-#pragma unroll
-        for (int j = 0; j < KB; ++j) {
-          if (j0 + j >= a.k) break;
-          any |= slots.g[j] != 0.f;
-          const int at = slots.e[j] - l * piece<T>();   // the column as seen from this lane's first
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const bool mine = at == i / piece<T>() * L * piece<T>() + i % piece<T>();
-            G[i] += mine ? slots.g[j] : 0.f;
-            if (kRenorm) n[i] += mine ? 1.f : 0.f;
-          }
-        }
-      }
-    }
-    softmax_row<V>(p, L);
-    if (gates && kRenorm) {
-      // over the selected experts alone: w = p / z, their gradient w (g - sum w g)
-      float z = 0.f, wg = 0.f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        z = fmaf(p[i], n[i], z);
-        wg = fmaf(p[i], G[i], wg);
-      }
-      z = group_sum(z, L);
-      wg = group_sum(wg, L);
-      const float inv = z == 0.f ? 0.f : __fdiv_rn(1.f, z);
-      wg *= inv;
-#pragma unroll
-      for (int i = 0; i < V; ++i) G[i] = p[i] * inv * (G[i] - n[i] * wg);
-    }
+    bool in = false;
     if (a.counts) {
       while (a.off && s < a.S && a.off[s + 1] <= tr) ++s;
-      const bool in = s < a.S && (!a.mask || a.mask[tr]);
+      in = s < a.S && (!a.mask || a.mask[tr]);
       if (in && held != s) {
         held = s;
-        const float c = __ldg(a.coef + s) * d_loss;
+        c_s = __ldg(a.coef + s) * d_loss;
         const int32_t* cnt = a.counts + static_cast<size_t>(s) * E;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const int e = column<T>(i, L, l);
-          bal[i] = e < E ? c * static_cast<float>(__ldg(cnt + e)) : 0.f;
+          const int c = column<T>(i, L, l);
+          bal[i] = c < E ? c_s * static_cast<float>(__ldg(cnt + c)) : 0.f;
         }
       }
-      any |= in;
-      if (gates && kRenorm) {   // p (b - sum b p) beside the gates' gradient
-        float dot = 0.f;
+    }
+    // something to differentiate: else the row's gradient is 0 whatever its logits hold
+    const bool any = group_max(g[0] != 0.f || g[1] != 0.f ? 1.f : 0.f, L) != 0.f || in;
+    softmax_row<V>(p, L, m, inv);
+    float dot = 0.f;   // sum of p times what it is multiplied with: the loss's part, and the raw gates'
 #pragma unroll
-        for (int i = 0; i < V; ++i) dot = fmaf(p[i], in ? bal[i] : 0.f, dot);
-        dot = group_sum(dot, L);
+    for (int i = 0; i < V; ++i) dot = fmaf(p[i], bal[i], dot);
+    dot = in ? dot * inv : 0.f;
+    float ps[2], z = 0.f, wg = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) G[i] = fmaf(p[i], (in ? bal[i] : 0.f) - dot, G[i]);
+    for (int u = 0; u < 2; ++u) {
+      ps[u] = e[u] >= 0 ? __expf(x[u] - m) * inv : 0.f;
+      if (kRenorm) {
+        z += ps[u];
+        wg += e[u] >= 0 ? ps[u] * g[u] : 0.f;
       } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) G[i] += in ? bal[i] : 0.f;
+        dot += e[u] >= 0 ? ps[u] * g[u] : 0.f;
       }
     }
-    if (!(gates && kRenorm)) {
-      float dot = 0.f;
+    dot = group_sum(dot, L);
+    // the gradients of every slot that chose the same expert (one, as the router gives them)
+    float gs[2] = {0.f, 0.f}, ns[2] = {0.f, 0.f};
+    if (gates) {
+      for (int j = 0; j < k; ++j) {
+        const int from = (lane & ~(L - 1)) | (j & (L - 1));
+        const int ej = __shfl_sync(0xffffffffu, j < L ? e[0] : e[1], from);
+        const float gj = __shfl_sync(0xffffffffu, j < L ? g[0] : g[1], from);
 #pragma unroll
-      for (int i = 0; i < V; ++i) dot = fmaf(p[i], G[i], dot);
-      dot = group_sum(dot, L);
-#pragma unroll
-      for (int i = 0; i < V; ++i) G[i] = p[i] * (G[i] - dot);
+        for (int u = 0; u < 2; ++u) {
+          gs[u] += ej == e[u] ? gj : 0.f;
+          if (kRenorm) ns[u] += ej == e[u] ? 1.f : 0.f;
+        }
+      }
     }
-    if (!live) continue;
-    OT* row = out + static_cast<size_t>(t) * E;
+    float inv_z = 0.f;
+    if (kRenorm && gates) {   // over the selected experts alone: w = p / z, their gradient w (g - sum w g)
+      z = group_sum(z, L);
+      wg = group_sum(wg, L);
+      inv_z = z == 0.f ? 0.f : __fdiv_rn(1.f, z);
+      wg *= inv_z;
+    }
+    OT* o = out + static_cast<size_t>(tr) * E;
 #pragma unroll
     for (int q = 0; q < V / piece<T>(); ++q) {
       constexpr int C = piece<T>();
       const int c = (q * L + l) * C;
       float v[C];
 #pragma unroll
-      for (int u = 0; u < C; ++u) v[u] = any ? G[q * C + u] : 0.f;
+      for (int u = 0; u < C; ++u) {
+        const int i = q * C + u;
+        v[u] = any ? p[i] * inv * ((in ? bal[i] : 0.f) - dot) : 0.f;
+      }
       if (a.vec) {
-        if (c < E) store_run<OT, C>(row + c, v);
+        if (live && c < E) store_run<OT, C>(o + c, v);
       } else {
 #pragma unroll
         for (int u = 0; u < C; ++u)
-          if (c + u < E) row[c + u] = from_f32(v[u], OT());
+          if (live && c + u < E) o[c + u] = from_f32(v[u], OT());
+      }
+    }
+    if (gates) {
+      __syncwarp();   // the selected entries come after the row's
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (!live || !any || e[u] < 0) continue;
+        const float be = in ? c_s * static_cast<float>(__ldg(a.counts + static_cast<size_t>(s) * E + e[u])) : 0.f;
+        float v;
+        if (kRenorm)
+          v = fmaf(ps[u] * inv_z, gs[u] - ns[u] * wg, ps[u] * (be - dot));
+        else
+          v = ps[u] * (be + gs[u] - dot);
+        o[e[u]] = from_f32(v, OT());
       }
     }
   }
@@ -566,7 +571,7 @@ int lanes_for(int E, int V) {  // lanes of a row: a power of two, V columns each
   while (L < 32 && L * V < E) L *= 2;
   return L;
 }
-int values_for(int E) { return E <= 256 ? 8 : 32; }
+int values_for(int E) { return E <= 512 ? 16 : 32; }
 
 int balance_chunk(int T) {
   if (T <= kBalSmall) return T > 0 ? (T + kFinCluster - 1) / kFinCluster : 1;
@@ -580,19 +585,19 @@ int launch_partial(const BalanceArgs& a, int V, int cols, int w, cudaStream_t s)
   const dim3 grid(a.chunks), block(kBalThreads);
   if (a.T <= kBalSmall) {
     const dim3 one(kFinCluster);
-    if (V == 8) return launch_pdl(__func__, balance_small_kernel<T, 8>, one, block, smem, s, a, cols, w);
+    if (V == 16) return launch_pdl(__func__, balance_small_kernel<T, 16>, one, block, smem, s, a, cols, w);
     return launch_pdl(__func__, balance_small_kernel<T, 32>, one, block, smem, s, a, cols, w);
   }
-  if (V == 8) return launch_pdl(__func__, balance_partial_kernel<T, 8>, grid, block, smem, s, a);
+  if (V == 16) return launch_pdl(__func__, balance_partial_kernel<T, 16>, grid, block, smem, s, a);
   return launch_pdl(__func__, balance_partial_kernel<T, 32>, grid, block, smem, s, a);
 }
 
 template <typename T, typename OT>
 int launch_grad(const RouterGradArgs& a, int V, int grid, cudaStream_t s) {
   const dim3 g(grid), b(kBalThreads);
-  if (V == 8)
-    return a.renorm ? launch_pdl(__func__, router_backward_kernel<T, OT, 8, true>, g, b, 0, s, a)
-                    : launch_pdl(__func__, router_backward_kernel<T, OT, 8, false>, g, b, 0, s, a);
+  if (V == 16)
+    return a.renorm ? launch_pdl(__func__, router_backward_kernel<T, OT, 16, true>, g, b, 0, s, a)
+                    : launch_pdl(__func__, router_backward_kernel<T, OT, 16, false>, g, b, 0, s, a);
   return a.renorm ? launch_pdl(__func__, router_backward_kernel<T, OT, 32, true>, g, b, 0, s, a)
                   : launch_pdl(__func__, router_backward_kernel<T, OT, 32, false>, g, b, 0, s, a);
 }
@@ -636,7 +641,7 @@ int launch_balance_loss(const void* logits, int dtype, const int32_t* idx, int T
   int cols = 8;
   while (cols * kFinCluster < E) cols *= 2;
   int w = 1;
-  while (w * cols < threads && w * 8 < a.chunks / S + 1) w *= 2;
+  while (w < 32 && w * cols < threads && w * 8 < a.chunks / S + 1) w *= 2;
   const int st = dtype == MOE_F32   ? launch_partial<float>(a, V, cols, w, s)
                  : dtype == MOE_F16 ? launch_partial<__half>(a, V, cols, w, s)
                                     : launch_partial<__nv_bfloat16>(a, V, cols, w, s);
@@ -653,6 +658,7 @@ int launch_router_backward(const void* logits, int dtype, const int32_t* idx, co
   a.logits = logits, a.idx = idx, a.d_w = d_w, a.T = T, a.E = E, a.k = k, a.renorm = renorm, a.off = off, a.S = S;
   a.mask = mask, a.counts = counts, a.coef = coef, a.d_loss = d_loss, a.out = out;
   a.L = lanes_for(E, V);
+  while (a.L * 2 < k) a.L *= 2;   // two slots to a lane
   a.vec = E % (dtype == MOE_F32 ? 4 : 8) == 0;   // then rows of every output type are stored whole too
   const int groups = kBalThreads / a.L;
   const int blocks = num_sms() * 3;   // one wave
