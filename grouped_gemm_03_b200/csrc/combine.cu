@@ -129,6 +129,21 @@ __device__ __forceinline__ void load_grad(const float* p, float (&g)[8]) {
   g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w, g[4] = b.x, g[5] = b.y, g[6] = b.z, g[7] = b.w;
 }
 
+// rows that this kernel reads once, and writes for another kernel to read
+__device__ __forceinline__ uint4 load_once(const __nv_bfloat16* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void store_once(__nv_bfloat16* p, const float (&f)[8]) {
+  __nv_bfloat162 h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+  __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<uint4*>(h));
+}
+
 // S: slots of one sweep over the columns (1, 2, 4 or 8); more slots take more sweeps
 template <typename GT, int S>
 __global__ void __launch_bounds__(256) combine_backward_kernel(
@@ -160,11 +175,24 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(
     for (int c = tid * 8; c < d; c += blockDim.x * 8) {
       float g[8];
       load_grad(g_row + c, g);
+      uint4 y[S];
       if (dw) {
-        uint4 y[S];
 #pragma unroll
         for (int u = 0; u < S; ++u)
-          y[u] = row[u] >= 0 ? __ldg(reinterpret_cast<const uint4*>(Y + row[u] * d + c)) : make_uint4(0, 0, 0, 0);
+          y[u] = row[u] >= 0 ? load_once(Y + row[u] * d + c) : make_uint4(0, 0, 0, 0);
+      }
+      if (dY) {  // needs dout alone: these go out while the rows of Y come in
+#pragma unroll
+        for (int u = 0; u < S; ++u) {
+          if (row[u] < 0) continue;
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = wj[u] * g[i];
+          store_once(dY + row[u] * d + c, v);
+        }
+        if (shared_row && j0 == 0) store_once(shared_row + c, g);
+      }
+      if (dw) {
 #pragma unroll
         for (int u = 0; u < S; ++u) {
           float f[8];
@@ -172,17 +200,6 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(
 #pragma unroll
           for (int i = 0; i < 8; ++i) dot[u] = fmaf(f[i], g[i], dot[u]);
         }
-      }
-      if (dY) {
-#pragma unroll
-        for (int u = 0; u < S; ++u) {
-          if (row[u] < 0) continue;
-          float v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = wj[u] * g[i];
-          store8(dY + row[u] * d + c, v);
-        }
-        if (shared_row && j0 == 0) store8(shared_row + c, g);
       }
     }
     if (!dw) continue;
