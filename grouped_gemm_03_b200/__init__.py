@@ -82,7 +82,8 @@ _SIGS = {
     "moe_router_backward": (_i, [_vp, _i, _ip, _fp, _i, _i, _i, _i, _ip, _i, _vp, _ip, _fp, _fp, _vp, _i, _vp]),
     "moe_adapter_plan_workspace_size": (_sz, [_i, _i]),
     "moe_adapter_plan": (_i, [_ip, _i, _i, _ip, _ip, _vp, _sz, _vp]),
-    "moe_lora": (_i, [_vp, _vp, _vp, _fp, _ip, _ip, _i, _i, _i, _i, _i, _vp, _vp, _i, _fp, _vp]),
+    "moe_lora_workspace_size": (_sz, [_i] * 5),
+    "moe_lora": (_i, [_vp, _vp, _vp, _fp, _ip, _ip, _i, _i, _i, _i, _i, _vp, _vp, _i, _fp, _vp, _sz, _vp]),
     "moe_lora_backward_workspace_size": (_sz, [_i] * 5),
     "moe_lora_backward": (_i, [_vp, _vp, _fp, _vp, _vp, _fp, _ip, _ip, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _i,
                                _vp, _sz, _vp]),
@@ -482,14 +483,14 @@ def adapter_plan(row_adapter, n: int, ws=None, stream=None):
 
 
 def lora(x, A, B, offsets, order, scale=None, base=None, out_dtype=torch.bfloat16, out=None, want_h: bool = False,
-         stream=None):
+         ws=None, stream=None):
     """base + scale (x A^T) B^T, each row with its own adapter (moe_lora); with want_h also h = x A^T [rows, R] fp32.
 
     A [n, R, d], B [n, N, R] bf16; offsets, order: adapter_plan's; base [rows, N] or None (0).  out=base adds
     in place.  Without `out` the result has base's type, or out_dtype."""
     if stream is not None:
         with torch.cuda.stream(stream):
-            return lora(x, A, B, offsets, order, scale, base, out_dtype, out, want_h)
+            return lora(x, A, B, offsets, order, scale, base, out_dtype, out, want_h, ws)
     dev = _device(x)
     rows, d = x.shape
     n, R, _ = A.shape
@@ -506,8 +507,12 @@ def lora(x, A, B, offsets, order, scale=None, base=None, out_dtype=torch.bfloat1
     p_base = _held(dev, base, "base", (out.dtype,), (rows, N))
     h = x.new_empty((rows, R), dtype=torch.float32) if want_h else None
     L = lib()
+    need = L.moe_lora_workspace_size(rows, n, d, N, R)
+    if need or ws is not None:
+        ws = _workspace(x, ws, need)
     st = L.moe_lora(p_x, p_A, p_B, p_s, p_off, p_ord, n, rows, d, N, R, p_base, p_out, _TORCH_DT[out.dtype],
-                    h.data_ptr() if want_h else None, _stream_of(dev))
+                    h.data_ptr() if want_h else None, None if ws is None else ws.data_ptr(),
+                    0 if ws is None else ws.numel(), _stream_of(dev))
     _check(st, "moe_lora")
     return (out, h) if want_h else out
 

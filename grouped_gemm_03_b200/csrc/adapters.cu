@@ -24,6 +24,7 @@
 
 #include "common.cuh"
 #include "lora.cuh"
+#include "lora_tc.cuh"
 
 namespace moe {
 namespace {
@@ -364,16 +365,14 @@ int launch_lora_tile(const LoraArgs& p, int cs, cudaStream_t s) {
 
 template <int RP, typename OT>
 int launch_lora_rows(LoraArgs& p, cudaStream_t s) {
-  const bool wide = p.rows > 16ll * p.n;  // more than one 16-row tile to an adapter
-  const int mt = wide ? 64 : 16;
   // CTAs to fill the SMs twice, each with at least 128 columns of the wider side
-  const long long tiles = static_cast<long long>(p.rows) / mt + p.n;
+  const long long tiles = static_cast<long long>(p.rows) / 16 + p.n;
   const int widest = p.d > p.N ? p.d : p.N;
   int cs = 1;
   while (cs < 8 && tiles * cs < 4ll * num_sms() && widest >= cs * 2 * 128) cs *= 2;
   p.kslice = ((p.d + cs - 1) / cs + 31) / 32 * 32;
   p.nslice = ((p.N + cs - 1) / cs + 31) / 32 * 32;
-  return wide ? launch_lora_tile<RP, 64, OT>(p, cs, s) : launch_lora_tile<RP, 16, OT>(p, cs, s);
+  return launch_lora_tile<RP, 16, OT>(p, cs, s);
 }
 
 template <typename OT>
@@ -407,15 +406,40 @@ int launch_adapter_plan(const int32_t* adapter, int rows, int n, int32_t* offset
                     static_cast<const int32_t*>(cnt), static_cast<const int32_t*>(err), offsets, order, status);
 }
 
-int launch_lora(const void* x, const void* A, const void* B, const float* scale, const int32_t* offsets,
-                const int32_t* order, int n, int rows, int d, int N, int R, const void* base, void* out, int out_dtype,
-                float* h_out, cudaStream_t s) {
-  if (rows == 0) return MOE_OK;
+// More than one 16-row tile to an adapter
+bool lora_two_launches(int rows, int n) { return rows > 16ll * n; }
+
+size_t lora_workspace_bytes(int rows, int n, int R) {
+  return lora_two_launches(rows, n) ? 256 + static_cast<size_t>(rows) * R * 4 : 0;
+}
+
+int launch_lora(const LoraForwardArgs& q, cudaStream_t s) {
+  if (q.rows == 0) return MOE_OK;
+  if (lora_two_launches(q.rows, q.n)) {
+    int* status = static_cast<int*>(q.ws);
+    float* h = reinterpret_cast<float*>(static_cast<char*>(q.ws) + 256);
+    StreamArgs p{};
+    p.X = static_cast<const __nv_bfloat16*>(q.x), p.M = static_cast<const __nv_bfloat16*>(q.A);
+    p.offsets = q.offsets, p.order = q.order, p.n = q.n, p.rows = q.rows, p.W = q.d, p.R = q.R;
+    p.proj = h, p.h_out = q.h_out, p.status = status;
+    // slices of a row: to give every SM two CTAs, up to the portable cluster
+    const long long tiles = static_cast<long long>(q.rows) / 128 + q.n;
+    p.chunk = 128, p.cluster = 1;
+    while (p.cluster < 8 && tiles * p.cluster < 2ll * num_sms() && q.d > p.cluster * 128) p.cluster *= 2;
+    p.cols = ((q.d + p.cluster - 1) / p.cluster + 127) / 128 * 128;
+    const int st = launch_lora_stream(p, kStreamProject, s);
+    if (st != MOE_OK) return st;
+    ExpandArgs e{};
+    e.h = h, e.M = static_cast<const __nv_bfloat16*>(q.B), e.scale = q.scale, e.offsets = q.offsets, e.order = q.order;
+    e.n = q.n, e.rows = q.rows, e.N = q.N, e.R = q.R, e.base = q.base, e.out = q.out, e.h_out = q.h_out;
+    e.status = status;
+    return launch_lora_expand(e, false, q.out_dtype, s);
+  }
   LoraArgs p{};
-  p.x = static_cast<const __nv_bfloat16*>(x), p.A = static_cast<const __nv_bfloat16*>(A);
-  p.B = static_cast<const __nv_bfloat16*>(B), p.scale = scale, p.offsets = offsets, p.order = order;
-  p.n = n, p.rows = rows, p.d = d, p.N = N, p.R = R, p.base = base, p.out = out, p.h_out = h_out;
-  return out_dtype == MOE_F32 ? launch_lora_rank<float>(p, s) : launch_lora_rank<__nv_bfloat16>(p, s);
+  p.x = static_cast<const __nv_bfloat16*>(q.x), p.A = static_cast<const __nv_bfloat16*>(q.A);
+  p.B = static_cast<const __nv_bfloat16*>(q.B), p.scale = q.scale, p.offsets = q.offsets, p.order = q.order;
+  p.n = q.n, p.rows = q.rows, p.d = q.d, p.N = q.N, p.R = q.R, p.base = q.base, p.out = q.out, p.h_out = q.h_out;
+  return q.out_dtype == MOE_F32 ? launch_lora_rank<float>(p, s) : launch_lora_rank<__nv_bfloat16>(p, s);
 }
 
 }  // namespace moe

@@ -173,9 +173,22 @@ int launch_router_backward(const void* logits, int dtype, const int32_t* idx, co
 size_t adapter_plan_workspace_bytes(int rows, int n);
 int launch_adapter_plan(const int32_t* adapter, int rows, int n, int32_t* offsets, int32_t* order, void* ws,
                         cudaStream_t s);
-int launch_lora(const void* x, const void* A, const void* B, const float* scale, const int32_t* offsets,
-                const int32_t* order, int n, int rows, int d, int N, int R, const void* base, void* out, int out_dtype,
-                float* h_out, cudaStream_t s);
+struct LoraForwardArgs {
+  const void* x;
+  const void* A;
+  const void* B;
+  const float* scale;
+  const int32_t* offsets;
+  const int32_t* order;
+  int n, rows, d, N, R;
+  const void* base;
+  void* out;
+  int out_dtype;
+  float* h_out;
+  void* ws;
+};
+size_t lora_workspace_bytes(int rows, int n, int R);
+int launch_lora(const LoraForwardArgs& a, cudaStream_t s);
 struct LoraBackwardArgs {
   const void* dC;
   const void* x;

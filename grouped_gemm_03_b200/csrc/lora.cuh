@@ -169,6 +169,12 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   const float ha = __uint_as_float(hi << 16), hb = __uint_as_float(hi & 0xffff0000u);
   lo = pack2(isfinite(ha) ? a - ha : 0.f, isfinite(hb) ? b - hb : 0.f);
 }
+// As three terms: hi + mid + lo are all 24 bits of a finite value.
+__device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  hi = pack2(a, b);
+  const float ha = __uint_as_float(hi << 16), hb = __uint_as_float(hi & 0xffff0000u);
+  split2(isfinite(ha) ? a - ha : 0.f, isfinite(hb) ? b - hb : 0.f, mid, lo);
+}
 __device__ __forceinline__ void split_store(__nv_bfloat16* hi, __nv_bfloat16* lo, float4 v, float s) {
   uint32_t h0, l0, h1, l1;
   split2(v.x * s, v.y * s, h0, l0);

@@ -478,9 +478,14 @@ int moe_adapter_plan(const int32_t* row_adapter, int rows, int n, int32_t* offse
   return launch_adapter_plan(row_adapter, rows, n, offsets, order, ws, as_stream(stream));
 }
 
+size_t moe_lora_workspace_size(int rows, int n, int d, int N, int R) {
+  if (check_adapter_shape(n, rows, d, N, R) != MOE_OK) return 0;
+  return lora_workspace_bytes(rows, n, R);
+}
+
 int moe_lora(const void* x, const void* A, const void* B, const float* scale, const int32_t* offsets,
              const int32_t* order, int n, int rows, int d, int N, int R, const void* base, void* out, int out_dtype,
-             float* h_out, void* stream) {
+             float* h_out, void* ws, size_t ws_bytes, void* stream) {
   const int st = check_adapter_shape(n, rows, d, N, R);
   if (st != MOE_OK) return st;
   if (out_dtype != MOE_F32 && out_dtype != MOE_BF16) return MOE_ERR_INVALID;
@@ -489,8 +494,13 @@ int moe_lora(const void* x, const void* A, const void* B, const float* scale, co
   if (!aligned(x, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(base, 16) || !aligned(out, 16) ||
       !aligned(h_out, 16))
     return MOE_ERR_INVALID;
-  return launch_lora(x, A, B, scale, offsets, order, n, rows, d, N, R, base, out, out_dtype, h_out,
-                     as_stream(stream));
+  const size_t need = lora_workspace_bytes(rows, n, R);
+  if (need > 0 && (!ws || !aligned(ws, 256) || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  LoraForwardArgs a{};
+  a.x = x, a.A = A, a.B = B, a.scale = scale, a.offsets = offsets, a.order = order;
+  a.n = n, a.rows = rows, a.d = d, a.N = N, a.R = R;
+  a.base = base, a.out = out, a.out_dtype = out_dtype, a.h_out = h_out, a.ws = ws;
+  return launch_lora(a, as_stream(stream));
 }
 
 size_t moe_lora_backward_workspace_size(int rows, int n, int d, int N, int R) {

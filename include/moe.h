@@ -384,7 +384,8 @@ int moe_adapter_plan(const int32_t* row_adapter, int rows, int n, int32_t* offse
                      size_t ws_bytes, void* stream);
 
 /* out[r] = base[r] + scale[a] * (x[r] A[a]^T) B[a]^T for the rows of adapter a,
- * out[r] = base[r] for the rows without one; one launch.
+ * out[r] = base[r] for the rows without one; one launch for a few rows to an
+ * adapter, two on the tensor cores for more.
  *   x      [rows, d] MOE_BF16;  A [n, R, d], B [n, N, R] MOE_BF16;  scale [n] fp32 or NULL (1)
  *   offsets, order  the plan (DEVICE arrays; entries outside their range are
  *          skipped, nothing outside the buffers is read or written)
@@ -393,12 +394,15 @@ int moe_adapter_plan(const int32_t* row_adapter, int rows, int n, int32_t* offse
  *          rows without an adapter are then not touched
  *   h_out  [rows, R] fp32: x A^T (0 for rows without an adapter), which
  *          moe_lora_backward takes, or NULL
- * fp32 sums, rounded once to out_dtype.  R a multiple of 8, 8 <= R <= 128
+ *   ws     moe_lora_workspace_size(...) bytes (status + h); where that is 0, NULL
+ * fp32 sums, rounded once to out_dtype.  Status word (where there is a
+ * workspace): MOE_ERR_TIMEOUT.  R a multiple of 8, 8 <= R <= 128
  * (pad smaller ranks with zeros); d % 8 == 0, N % 8 == 0; x, A, B, base, out
  * and h_out 16-byte aligned; out must not overlap x. */
+size_t moe_lora_workspace_size(int rows, int n, int d, int N, int R);
 int moe_lora(const void* x, const void* A, const void* B, const float* scale, const int32_t* offsets,
              const int32_t* order, int n, int rows, int d, int N, int R, const void* base, void* out, int out_dtype,
-             float* h_out, void* stream);
+             float* h_out, void* ws, size_t ws_bytes, void* stream);
 
 /* Gradient of moe_lora, from dC = d out and the h that the forward kept:
  *   dh[r] = scale[a] * dC[r] B[a]
@@ -408,8 +412,8 @@ int moe_lora(const void* x, const void* A, const void* B, const float* scale, co
  *   dx_base [rows, d] dx_dtype (the projection's own input gradient) or NULL (0)
  *   dx      [rows, d] dx_dtype (MOE_BF16 | MOE_F32) or NULL (not wanted); may be dx_base itself
  *   dA [n, R, d], dB [n, N, R] grad_dtype (MOE_F32 | MOE_BF16), each or NULL; one of dx, dA, dB is given
- *   ws      moe_lora_backward_workspace_size(...) bytes (dh and partial sums; no status word)
- * Sums run in a fixed order.  Shapes and alignment as for moe_lora; dx must
+ *   ws      moe_lora_backward_workspace_size(...) bytes (status + dh and partial sums)
+ * Status word: MOE_ERR_TIMEOUT.  Sums run in a fixed order.  Shapes and alignment as for moe_lora; dx must
  * not overlap dC or x. */
 size_t moe_lora_backward_workspace_size(int rows, int n, int d, int N, int R);
 int moe_lora_backward(const void* dC, const void* x, const float* h, const void* A, const void* B, const float* scale,

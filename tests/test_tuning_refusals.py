@@ -57,8 +57,9 @@ def test_adapter_plan(L):
     assert call(P, 10, 2, P, P, P, L.moe_adapter_plan_workspace_size(10, 2) - 1, NULL) == WORKSPACE
 
 
-def _lora(L, x=P, A=P, B=P, off=P, order=P, n=2, rows=10, d=64, N=64, R=8, base=NULL, out=Q, dt=2):
-    return L.moe_lora(x, A, B, NULL, off, order, n, rows, d, N, R, base, out, dt, NULL, NULL)
+def _lora(L, x=P, A=P, B=P, off=P, order=P, n=2, rows=10, d=64, N=64, R=8, base=NULL, out=Q, dt=2, ws=NULL,
+          nb=0):
+    return L.moe_lora(x, A, B, NULL, off, order, n, rows, d, N, R, base, out, dt, NULL, ws, nb, NULL)
 
 
 def test_lora(L):
@@ -71,6 +72,11 @@ def test_lora(L):
         assert _lora(L, **{name: NULL}) == INVALID
     for name in ("x", "A", "B", "base", "out"):
         assert _lora(L, **{name: ODD}) == INVALID
+    need = L.moe_lora_workspace_size(1000, 2, 64, 64, 8)
+    assert need > 0 and L.moe_lora_workspace_size(10, 2, 64, 64, 8) == 0
+    assert L.moe_lora_workspace_size(1000, 2, 64, 64, 20) == 0
+    assert _lora(L, rows=1000) == WORKSPACE and _lora(L, rows=1000, ws=P, nb=need - 1) == WORKSPACE
+    assert _lora(L, rows=1000, ws=ODD, nb=BIG) == WORKSPACE
 
 
 def _back(L, dC=P, x=P, h=P, n=2, rows=10, d=64, N=64, R=8, dx=Q, dxt=2, dA=Q, dB=Q, gt=0, ws=P, nb=BIG):
