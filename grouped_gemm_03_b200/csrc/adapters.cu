@@ -422,10 +422,10 @@ int launch_lora(const LoraForwardArgs& q, cudaStream_t s) {
     p.X = static_cast<const __nv_bfloat16*>(q.x), p.M = static_cast<const __nv_bfloat16*>(q.A);
     p.offsets = q.offsets, p.order = q.order, p.n = q.n, p.rows = q.rows, p.W = q.d, p.R = q.R;
     p.proj = h, p.h_out = q.h_out, p.status = status;
-    // slices of a row: to give every SM two CTAs, up to the portable cluster
+    // slices of a row: as many as leave two CTAs to an SM, up to the portable cluster
     const long long tiles = static_cast<long long>(q.rows) / 128 + q.n;
     p.chunk = 128, p.cluster = 1;
-    while (p.cluster < 8 && tiles * p.cluster < 2ll * num_sms() && q.d > p.cluster * 128) p.cluster *= 2;
+    while (p.cluster < 8 && tiles * p.cluster <= num_sms() && q.d > p.cluster * 128) p.cluster *= 2;
     p.cols = ((q.d + p.cluster - 1) / p.cluster + 127) / 128 * 128;
     const int st = launch_lora_stream(p, kStreamProject, s);
     if (st != MOE_OK) return st;

@@ -5,7 +5,7 @@
 // out cross HBM once, so the kernel is a copy with a small product in its
 // middle.  A CTA takes up to 128 rows of one adapter and a slice of the
 // columns, 64 at a time: warps 0-3 bring the base tile and the adapter's
-// columns (cp.async into a ring of stages), one thread of warp 8 issues the
+// columns (TMA, the rows by gather4, into a ring of stages), one thread of warp 12 issues the
 // 128 x 64 MMAs into one of two accumulators, warps 4-7 add the accumulator to
 // the base tile in shared memory, where a thread holds a row, and write it out
 // from there, where 8 neighbouring lanes hold one: full 128-byte lines both
@@ -25,7 +25,9 @@
 namespace moe {
 namespace {
 
-constexpr int kExpandThreads = 288;
+constexpr int kLoaders = 128, kDrainers = 256;
+constexpr int kExpandThreads = kLoaders + kDrainers + 32;
+constexpr int kMmaWarp = kExpandThreads / 32 - 1;
 constexpr int kRows = 128;
 constexpr int kBC = 64;  // columns of a block
 
@@ -46,14 +48,12 @@ struct ExpandCfg {
 
 template <int RP, bool KN, typename OT>
 __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
-    lora_expand_kernel(const ExpandArgs p) {
+    lora_expand_kernel(const ExpandArgs p, const __grid_constant__ CUtensorMap map_base,
+                       const __grid_constant__ CUtensorMap map_m) {
   using C = ExpandCfg<RP, KN, OT>;
   constexpr int S = C::STAGES;
   constexpr int VEC = 16 / sizeof(OT);          // values of a 16-byte piece
   constexpr int PIECES = kBC / VEC;             // of a row's block: 8 or 16
-  constexpr int PER = kRows * PIECES / 128;     // a thread's
-  pdl_wait();
-  pdl_launch_dependents();
   extern __shared__ uint8_t s_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_h = smem + S * C::STAGE;
@@ -64,6 +64,22 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
   volatile int* abort_flag = &s_abort;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      ptx::mbar_init(&full[i], 1);
+      ptx::mbar_init(&empty[i], kDrainers);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&acc_full[i], 1);
+      ptx::mbar_init(&acc_free[i], kDrainers);
+    }
+    ptx::mbar_init(&h_full, kDrainers);
+    ptx::mbar_init(&drained, 1);
+    s_abort = 0;
+    ptx::fence_mbar_init();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
   int a, start, end;
   if (!find_tile(p.offsets, p.n, p.rows, kRows, blockIdx.x, a, start, end)) return;
   const int N = p.N, R = p.R;
@@ -93,23 +109,20 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
   }
   const int blocks = (col1 - col0 + kBC - 1) / kBC;
 
-  if (tid == 0) {
-    for (int i = 0; i < S; ++i) {
-      ptx::mbar_init(&full[i], 128);
-      ptx::mbar_init(&empty[i], 128);
-    }
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&acc_full[i], 1);
-      ptx::mbar_init(&acc_free[i], 128);
-    }
-    ptx::mbar_init(&h_full, 128);
-    ptx::mbar_init(&drained, 1);
-    s_abort = 0;
-    ptx::fence_mbar_init();
-  }
-  if (warp == 8) {
+  const int et = tid - kLoaders;
+  constexpr int NP = RP * 16 / kDrainers;   // a drainer's pieces of 8 ranks of h
+  float v[NP][8];
+  if (warp == kMmaWarp) {
     ptx::tmem_alloc(&s_tmem, 2 * kBC);
     ptx::tmem_relinquish();
+  } else if (et >= 0) {                     // h's loads are in flight across the setup
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int i = et + k * kDrainers, m = i / (RP / 8), j = i % (RP / 8) * 8;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[k][u] = 0.f;
+      if (start + m < end && j < R) load8(p.h + static_cast<size_t>(start + m) * R + j, v[k]);
+    }
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -120,79 +133,63 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
     if (p.status) set_status(p.status, MOE_ERR_TIMEOUT);
   };
 
-  if (warp < 4) {
-    // ---- base tiles and the adapter's columns
-    constexpr int LAG = S - 1;
-    auto hand_over = [&](int t) {
-      ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(&full[t % S]);
-    };
-    const __nv_bfloat16* M = p.M + static_cast<size_t>(a) * N * R;
+  if (warp < kLoaders / 32) {
+    // ---- base tiles and the adapter's columns.  Lane l of a warp gathers its (l % 8)-th four rows, the
+    // (l / 8)-th 128 bytes of the block; a row that is not there is taken from behind base, as zeros.
+    constexpr int SUBS = kBC * sizeof(OT) / 128;
+    const int quad = warp * 8 + lane % 8, sub = lane / 8;
+    int row[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) row[u] = s_row[quad * 4 + u] >= 0 ? s_row[quad * 4 + u] : p.rows;
     bool ok = true;
-    for (int t = 0; t < blocks; ++t) {
-      if (t >= S && !ptx::mbar_wait(&empty[t % S], (t / S - 1) & 1, abort_flag, kWaitLimitNs)) {
+    int t = 0;
+    for (; t < blocks; ++t) {
+      if (t >= S && !ptx::mbar_wait_warp(&empty[t % S], (t / S - 1) & 1, abort_flag, kWaitLimitNs)) {
         give_up();
         ok = false;
         break;
       }
-      const uint32_t dst = ptx::smem_u32(smem + t % S * C::STAGE);
+      uint8_t* dst = smem + t % S * C::STAGE;
       const int col = col0 + t * kBC;
-      if (base) {
+      if (tid == 0) {
+        ptx::mbar_arrive_expect_tx(&full[t % S], C::WBYTES + (base ? C::BASE : 0));
+        if constexpr (KN) {  // rank j's row of 64 columns
+          tma_load_3d(dst + C::BASE, &map_m, &full[t % S], col, 0, a);
+        } else {             // column n's row of ranks
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int m = i * (128 / PIECES) + tid / PIECES, c = tid % PIECES;
-          const int r = s_row[m];
-          const bool in = r >= 0 && col + c * VEC < col1;
-          cp_async16z(dst + c / 8 * (kRows * 128) + swz(m, c % 8),
-                      in ? base + static_cast<size_t>(r) * N + col + c * VEC : base, in);
+          for (int h = 0; h < RP; h += 64)
+            tma_load_3d(dst + C::BASE + h / 64 * (kBC * 128), &map_m, &full[t % S], h, col, a);
         }
       }
-      const uint32_t w = dst + C::BASE;
-      if constexpr (KN) {  // rank j's row of 64 columns
-        for (int i = tid; i < RP * 8; i += 128) {
-          const int j = i / 8, c = i % 8;
-          const bool in = j < R && col + c * 8 < col1;
-          cp_async16z(w + swz(j, c), in ? M + static_cast<size_t>(j) * N + col + c * 8 : M, in);
-        }
-      } else {             // column n's row of ranks
-#pragma unroll
-        for (int i = tid; i < kBC * (RP / 8); i += 128) {
-          const int n = i / (RP / 8), c = i % (RP / 8);
-          const bool in = col + n < col1 && c * 8 < R;
-          cp_async16z(w + c / 8 * (kBC * 128) + swz(n, c % 8),
-                      in ? M + static_cast<size_t>(col + n) * R + c * 8 : M, in);
-        }
-      }
-      cp_commit();
-      if (t >= LAG) {
-        cp_wait<LAG>();
-        hand_over(t - LAG);
-      }
+      __syncwarp();
+      if (base && sub < SUBS)
+        ptx::tma_gather4(dst + sub * (kRows * 128) + quad * 512, &map_base, &full[t % S], col + sub * (128 / sizeof(OT)),
+                         row[0], row[1], row[2], row[3]);
     }
-    cp_wait<0>();
-    if (ok)
-      for (int u = blocks > LAG ? blocks - LAG : 0; u < blocks; ++u) hand_over(u);
-  } else if (warp < 8) {
+    if (!ok) {   // what is in flight lands before the block ends
+      int never = 0;
+      for (int u = t > S ? t - S : 0; u < t; ++u) ptx::mbar_wait_warp(&full[u % S], (u / S) & 1, &never, kWaitLimitNs);
+    }
+  } else if (warp < kMmaWarp) {
     // ---- h's terms in, then block by block: accumulator + base, out
-    const int et = tid - 128, ew = warp - 4;
-    const uint32_t lane_base = static_cast<uint32_t>(ew * 32) << 16;
+    const int ew = warp - kLoaders / 32, quarter = ew & 3, half = ew >> 2;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const float sc = p.scale ? __ldg(p.scale + a) : 1.f;
-    for (int i = et; i < kRows * (RP / 8); i += 128) {
-      const int m = i / (RP / 8), j = i % (RP / 8) * 8;
-      float v[8] = {};
-      if (start + m < end && j < R) load8(p.h + static_cast<size_t>(start + m) * R + j, v);
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int i = et + k * kDrainers, m = i / (RP / 8), j = i % (RP / 8) * 8;
       uint32_t w[3][4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         if constexpr (C::TERMS == 3)
-          split3(v[2 * u] * sc, v[2 * u + 1] * sc, w[0][u], w[1][u], w[2][u]);
+          split3(v[k][2 * u] * sc, v[k][2 * u + 1] * sc, w[0][u], w[1][u], w[2][u]);
         else
-          split2(v[2 * u] * sc, v[2 * u + 1] * sc, w[0][u], w[1][u]);
+          split2(v[k][2 * u] * sc, v[k][2 * u + 1] * sc, w[0][u], w[1][u]);
       }
 #pragma unroll
       for (int q = 0; q < C::TERMS; ++q) {
-        const int k = q * RP + j;
-        *reinterpret_cast<uint4*>(s_h + k / 64 * (kRows * 128) + swz(m, k % 64 / 8)) =
+        const int kk = q * RP + j;
+        *reinterpret_cast<uint4*>(s_h + kk / 64 * (kRows * 128) + swz(m, kk % 64 / 8)) =
             make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
       }
     }
@@ -207,48 +204,46 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
       }
       ptx::tc_fence_after();
       uint8_t* tile = smem + t % S * C::STAGE;
-      const int m = ew * 32 + lane;
-      const uint32_t from = tmem + lane_base + (t & 1) * kBC;
-#pragma unroll
-      for (int k = 0; k < kBC; k += 32) {
-        uint32_t r[32];
-        __syncwarp();
-        ptx::tmem_ld_32x32b_x32(from + k, r);
-        ptx::tmem_ld_wait();
-#pragma unroll
-        for (int u = 0; u < 32; u += VEC) {
-          const int c = (k + u) / VEC;
-          uint4* at = reinterpret_cast<uint4*>(tile + c / 8 * (kRows * 128) + swz(m, c % 8));
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (base) v = *at;
-          if constexpr (sizeof(OT) == 4) {
-            v.x = __float_as_uint(__uint_as_float(v.x) + __uint_as_float(r[u]));
-            v.y = __float_as_uint(__uint_as_float(v.y) + __uint_as_float(r[u + 1]));
-            v.z = __float_as_uint(__uint_as_float(v.z) + __uint_as_float(r[u + 2]));
-            v.w = __float_as_uint(__uint_as_float(v.w) + __uint_as_float(r[u + 3]));
-          } else {
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              w[q] = pack2(__uint_as_float(w[q] << 16) + __uint_as_float(r[u + 2 * q]),
-                           __uint_as_float(w[q] & 0xffff0000u) + __uint_as_float(r[u + 2 * q + 1]));
-            v = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-          *at = v;
-        }
-      }
+      const int m = quarter * 32 + lane;
+      uint32_t r[32];
+      __syncwarp();
+      ptx::tmem_ld_32x32b_x32(tmem + lane_base + (t & 1) * kBC + half * 32, r);
+      ptx::tmem_ld_wait();
       ptx::tc_fence_before();
       ptx::mbar_arrive(&acc_free[t & 1]);
+      constexpr int HP = PIECES / 2;                // pieces of half a row
+#pragma unroll
+      for (int u = 0; u < 32; u += VEC) {
+        const int c = half * HP + u / VEC;
+        uint4* at = reinterpret_cast<uint4*>(tile + c / 8 * (kRows * 128) + swz(m, c % 8));
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (base) x = *at;
+        if constexpr (sizeof(OT) == 4) {
+          x.x = __float_as_uint(__uint_as_float(x.x) + __uint_as_float(r[u]));
+          x.y = __float_as_uint(__uint_as_float(x.y) + __uint_as_float(r[u + 1]));
+          x.z = __float_as_uint(__uint_as_float(x.z) + __uint_as_float(r[u + 2]));
+          x.w = __float_as_uint(__uint_as_float(x.w) + __uint_as_float(r[u + 3]));
+        } else {
+          uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            w[q] = pack2(__uint_as_float(w[q] << 16) + __uint_as_float(r[u + 2 * q]),
+                         __uint_as_float(w[q] & 0xffff0000u) + __uint_as_float(r[u + 2 * q + 1]));
+          x = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        *at = x;
+      }
       __syncwarp();
       const int col = col0 + t * kBC;
 #pragma unroll
-      for (int i = 0; i < PIECES; ++i) {  // the warp's 32 rows, PIECES lanes to a row
-        const int q = ew * 32 + i * (32 / PIECES) + lane / PIECES, c = lane % PIECES;
-        const int r = s_row[q];
-        const uint4 v = *reinterpret_cast<const uint4*>(tile + c / 8 * (kRows * 128) + swz(q, c % 8));
-        if (r >= 0 && col + c * VEC < col1)
-          *reinterpret_cast<uint4*>(out + static_cast<size_t>(r) * N + col + c * VEC) = v;
+      for (int i = 0; i < HP; ++i) {                // the warp's 32 rows, HP lanes to a row
+        const int q = quarter * 32 + i * (32 / HP) + lane / HP, c = half * HP + lane % HP;
+        const int r2 = s_row[q];
+        const uint4 x = *reinterpret_cast<const uint4*>(tile + c / 8 * (kRows * 128) + swz(q, c % 8));
+        if (r2 >= 0 && col + c * VEC < col1)
+          *reinterpret_cast<uint4*>(out + static_cast<size_t>(r2) * N + col + c * VEC) = x;
       }
+      ptx::fence_proxy_async_smem();   // the tile was written to; the next one comes by TMA
       ptx::mbar_arrive(&empty[t % S]);
     }
   } else if (lane == 0) {
@@ -284,10 +279,26 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
   }
   __syncwarp();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kMmaWarp) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 2 * kBC);
   }
+}
+
+// base [rows, N] in pieces of one row and 128 bytes
+template <typename OT>
+bool make_row_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t N) {
+  if constexpr (sizeof(OT) == 2) return make_map(m, base, 2, rows, N, 1);
+  const EncodeTiledFn enc = get_encode_fn();
+  const cuuint64_t dims[2] = {N, rows}, strides[1] = {N * 4};
+  const cuuint32_t box[2] = {32, 1}, estr[2] = {1, 1};
+  if (!enc || enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
+    record_cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled rejected the base's layout");
+    return false;
+  }
+  return true;
 }
 
 template <int RP, bool KN, typename OT>
@@ -297,8 +308,13 @@ int launch_expand_tile(const ExpandArgs& p, cudaStream_t s) {
   auto kernel = lora_expand_kernel<RP, KN, OT>;
   const int st = allow_smem(done, kernel, C::SMEM);
   if (st != MOE_OK) return st;
+  CUtensorMap mb, mm;
+  if (!(KN ? make_adapter_map(&mm, p.M, p.n, p.R, p.N, RP, 64) : make_adapter_map(&mm, p.M, p.n, p.N, p.R, kBC, 64)))
+    return MOE_ERR_CUDA;
+  mb = mm;
+  if (p.base && !make_row_map<OT>(&mb, p.base, p.rows, p.N)) return MOE_ERR_CUDA;
   return launch_pdl("lora_expand_kernel", kernel, dim3(p.rows / kRows + p.n + 1, (p.N + p.cols - 1) / p.cols),
-                    dim3(kExpandThreads), C::SMEM, s, p);
+                    dim3(kExpandThreads), C::SMEM, s, p, mb, mm);
 }
 template <bool KN, typename OT>
 int launch_expand_rank(const ExpandArgs& p, cudaStream_t s) {
@@ -311,10 +327,10 @@ int launch_expand_rank(const ExpandArgs& p, cudaStream_t s) {
 }  // namespace
 
 int launch_lora_expand(ExpandArgs p, bool kn, int out_dtype, cudaStream_t s) {
-  // columns of a CTA: the widest slice (up to 1024) that still gives every SM two CTAs
+  // columns of a CTA: the narrowest slice (of 128 to 1024) with which two CTAs to an SM are all of them
   const long long tiles = static_cast<long long>(p.rows) / kRows + p.n;
   p.cols = 1024;
-  while (p.cols > 128 && tiles * ((p.N + p.cols - 1) / p.cols) < 2ll * num_sms()) p.cols /= 2;
+  while (p.cols > 128 && tiles * ((p.N + p.cols / 2 - 1) / (p.cols / 2)) <= 2ll * num_sms()) p.cols /= 2;
   if (out_dtype == MOE_F32) return kn ? launch_expand_rank<true, float>(p, s) : launch_expand_rank<false, float>(p, s);
   return kn ? launch_expand_rank<true, __nv_bfloat16>(p, s) : launch_expand_rank<false, __nv_bfloat16>(p, s);
 }

@@ -25,9 +25,21 @@
 // (an MMA of N <= 64 is bound by reading its A operand); above, one after the
 // other into the same accumulator.
 //
-// Warps 0-3 load X (rows are gathered through the plan's order, 16 bytes a
-// cp.async, swizzled by hand), 4-7 prepare V and empty TMEM, one thread of
-// warp 8 issues the MMAs.  Every wait has a time limit; one that runs out
+// Both V and B are read as they lie in memory, a row's ranks side by side: the
+// MMA takes them with the ranks along N and the rows along K (MN-major), so
+// nothing is transposed on the way.
+//
+// The first warps load X (tile::gather4, four rows of the plan's order at a
+// time, zeros for a row that is not there; the next 128 rows' ids are fetched a
+// step ahead), eight more prepare V, whose loads run a step ahead too, and
+// empty TMEM, one thread of the last warp issues the MMAs.  gather4 takes a
+// warp about 85 cycles, so eight warps an SM issue them: four where two CTAs
+// share it.  Measured on 117 MB in 224 CTAs: 1.7 TB/s from one warp an SM, 4.4
+// from four, 5.2 from eight, 5.7 from two CTAs of four; cp.async of 16 bytes by
+// the same warps reaches the same rates alone, but its address arithmetic and
+// proxy fences held the whole kernel to 3.5.  An MMA of up to 64 columns takes
+// 51 cycles whatever its N (its A operand comes from shared memory).
+// Every wait has a time limit; one that runs out
 // raises the block's abort flag, every role leaves its loop, copies and MMAs in
 // flight are waited for, TMEM is freed and MOE_ERR_TIMEOUT is left in *status.
 #include <cstdint>
@@ -39,7 +51,7 @@
 namespace moe {
 namespace {
 
-constexpr int kStreamThreads = 288;
+constexpr int kDrainers = 256;
 constexpr int kTile = 128;                 // rows and columns of a tile
 constexpr int kSub = kTile * 128;          // bytes of 128 rows x 64 columns
 constexpr int kTerms = 3;
@@ -54,45 +66,55 @@ struct StreamCfg {
   static constexpr int PCOL = GRAD ? BLOCKS * GCOLS : 0;                    // their first TMEM column
   static constexpr int USED = PCOL + (PROJ ? PBUF * RP : 0);
   static constexpr int TMEM = USED <= 32 ? 32 : USED <= 64 ? 64 : USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
-  static constexpr int MSUB = RP * 128;                                     // bytes of M for 64 columns
-  static constexpr int M_ALL = PROJ && GRAD ? BLOCKS * 2 * MSUB : 0;        // resident
-  static constexpr int V_SUB = GRAD ? kTerms * RP * 128 : 0;                // bytes of V's terms for 64 rows
+  static constexpr int MSUB = RP * 128;                                     // bytes of A's rows for 64 columns
+  static constexpr int RANKS = RankTile<RP>::BYTES;                         // 128 rows of RP ranks: V's term, B's block
+  static constexpr int M_ALL = PROJ && GRAD ? BLOCKS * RANKS : 0;           // resident
+  static constexpr int V_ALL = GRAD ? kTerms * RANKS : 0;
   static constexpr int STAGE = 2 * kSub + (PROJ && !GRAD ? 2 * MSUB : 0);
   static constexpr int PER_SM = RP <= 32 || (!GRAD && RP <= 64) ? 2 : 1;
+  static constexpr int LW = PER_SM == 2 ? 4 : 8;                            // warps that load
+  static constexpr int MMA_WARP = LW + kDrainers / 32;
+  static constexpr int THREADS = (MMA_WARP + 1) * 32;
+  static constexpr int GS = RP / 2 + 4;                                     // row stride of a warp's share of G on its way out
   static constexpr int BUDGET = PER_SM == 2 ? 110 * 1024 : 226 * 1024;
-  static constexpr int STAGES_RAW = (BUDGET - M_ALL - 2 * V_SUB) / STAGE;
+  static constexpr int STAGES_RAW = (BUDGET - M_ALL - V_ALL) / STAGE;
   static constexpr int STAGES = STAGES_RAW > 4 ? 4 : STAGES_RAW;
-  static constexpr int SMEM = STAGES * STAGE + M_ALL + 2 * V_SUB + 1024;    // + alignment slack
-  static_assert(USED <= 512 && STAGES >= 2 && (GRAD || kTile * PS * 4 <= STAGES * STAGE), "TMEM and shared memory");
+  static constexpr int SMEM = STAGES * STAGE + M_ALL + V_ALL + 1024;        // + alignment slack
+  static_assert(USED <= 512 && STAGES >= 2 && (GRAD || kTile * PS * 4 <= STAGES * STAGE) &&
+                    (kDrainers * GS * 4 <= STAGES * STAGE + M_ALL), "TMEM and shared memory");
 };
 
-// 16 accumulator columns from `col` on, the terms added up, smallest first
-template <bool STACK, int RP>
-__device__ __forceinline__ void load_grad16(uint32_t at, float (&v)[16]) {
-  uint32_t r[16];
-  ptx::tmem_ld_32x32b_x16(at, r);
+// N accumulator columns (8, 16 or 32), in flight until the wait
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[8]) { ptx::tmem_ld_32x32b_x8(at, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[16]) { ptx::tmem_ld_32x32b_x16(at, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[32]) { ptx::tmem_ld_32x32b_x32(at, r); }
+
+// N columns of G, the terms added up, smallest first
+template <bool STACK, int RP, int N>
+__device__ __forceinline__ void load_grad(uint32_t at, float (&v)[N]) {
+  uint32_t r[N];
+  tmem_ld(at, r);
   if constexpr (STACK) {
-    uint32_t s[16], t[16];
-    ptx::tmem_ld_32x32b_x16(at + RP, s);
-    ptx::tmem_ld_32x32b_x16(at + 2 * RP, t);
+    uint32_t s[N], t[N];
+    tmem_ld(at + RP, s);
+    tmem_ld(at + 2 * RP, t);
     ptx::tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      v[i] = __uint_as_float(r[i]) + (__uint_as_float(s[i]) + __uint_as_float(t[i]));
+    for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]) + (__uint_as_float(s[i]) + __uint_as_float(t[i]));
   } else {
     ptx::tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
   }
 }
 
 template <int RP, bool PROJ, bool GRAD>
-__global__ void __launch_bounds__(kStreamThreads, StreamCfg<RP, PROJ, GRAD>::PER_SM)
-    lora_stream_kernel(const StreamArgs p) {
+__global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<RP, PROJ, GRAD>::PER_SM)
+    lora_stream_kernel(const StreamArgs p, const __grid_constant__ CUtensorMap map_x,
+                       const __grid_constant__ CUtensorMap map_m) {
   using C = StreamCfg<RP, PROJ, GRAD>;
-  constexpr int S = C::STAGES;
-  pdl_wait();
-  pdl_launch_dependents();
+  using RT = RankTile<RP>;
+  constexpr int S = C::STAGES, kLoaders = C::LW * 32, kMmaWarp = C::MMA_WARP;
   extern __shared__ uint8_t s_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_m = smem + S * C::STAGE;
@@ -103,6 +125,22 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<RP, PROJ, GRAD>::PER
   volatile int* abort_flag = &s_abort;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      ptx::mbar_init(&full[i], 1);
+      ptx::mbar_init(&empty[i], 1);
+    }
+    ptx::mbar_init(&v_full, kDrainers);
+    ptx::mbar_init(&step_done[0], 1);
+    ptx::mbar_init(&step_done[1], 1);
+    ptx::mbar_init(&drained, 1);
+    ptx::mbar_init(&p_free[0], kDrainers);
+    ptx::mbar_init(&p_free[1], kDrainers);
+    s_abort = 0;
+    ptx::fence_mbar_init();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
   if (p.status && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *p.status = MOE_OK;
   const uint32_t CS = GRAD ? 1 : cluster_size();
   const int slot = GRAD ? blockIdx.x : blockIdx.x / CS, slice = GRAD ? blockIdx.y : cluster_rank();
@@ -115,38 +153,9 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<RP, PROJ, GRAD>::PER
   const int tiles = steps * blocks;
   const bool want_p = PROJ && p.proj, want_g = GRAD && p.grad;
 
-  if (tid == 0) {
-    for (int i = 0; i < S; ++i) {
-      ptx::mbar_init(&full[i], 128);
-      ptx::mbar_init(&empty[i], 1);
-    }
-    ptx::mbar_init(&v_full, 128);
-    ptx::mbar_init(&step_done[0], 1);
-    ptx::mbar_init(&step_done[1], 1);
-    ptx::mbar_init(&drained, 1);
-    ptx::mbar_init(&p_free[0], 128);
-    ptx::mbar_init(&p_free[1], 128);
-    s_abort = 0;
-    ptx::fence_mbar_init();
-  }
-  if (warp == 8) {
+  if (warp == kMmaWarp) {
     ptx::tmem_alloc(&s_tmem, C::TMEM);
     ptx::tmem_relinquish();
-  } else if (PROJ && GRAD) {
-    // M = B's slice, transposed on the way: rank j's row of 64 columns, for each 64
-    const __nv_bfloat16* src = p.M + static_cast<size_t>(a) * W * R;
-    for (int i = tid; i < blocks * kTile * (RP / 8); i += 256) {
-      const int n = i % (blocks * kTile), j = i / (blocks * kTile) * 8;
-      const bool in = col0 + n < W && j < R;
-      const uint4 v = in ? ldg16(src + static_cast<size_t>(col0 + n) * R + j) : make_uint4(0, 0, 0, 0);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      uint8_t* t = s_m + n / 64 * C::MSUB;
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-        *reinterpret_cast<uint16_t*>(t + swz(j + u, n % 64 / 8) + n % 8 * 2) =
-            static_cast<uint16_t>(w[u / 2] >> (u % 2 * 16));
-    }
-    ptx::fence_proxy_async_smem();
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -157,87 +166,115 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<RP, PROJ, GRAD>::PER
     if (p.status) set_status(p.status, MOE_ERR_TIMEOUT);
   };
 
-  if (warp < 4) {
-    // ---- X: tile t goes to stage t % S; what is landed is handed over S - 1 tiles later
-    constexpr int LAG = S - 1;
-    int row[16];
-    auto hand_over = [&](int t) {
-      ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(&full[t % S]);
+  if (warp < kLoaders / 32) {
+    // ---- X: tile t goes to stage t % S.  Lane l of a warp gathers its (l % Q)-th four rows, columns
+    // 64 (l / Q) .. + 63 of the tile's 128; a row that is not there is taken from behind X, as zeros.
+    constexpr int Q = 32 / C::LW;
+    const int quad = warp * Q + lane % Q, sub = lane / Q;
+    const bool mine = sub < 2;
+    int next[4], row[4];
+    auto fetch_ids = [&](int step) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int at = start + step * kTile + quad * 4 + u;
+        next[u] = mine && at < end ? __ldg(p.order + at) : -1;
+      }
     };
+    fetch_ids(0);
     bool ok = true;
     int t = 0;
     for (int step = 0; step < steps && ok; ++step) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int at = start + step * kTile + i * 8 + tid / 16;
-        const int r = at < end ? __ldg(p.order + at) : -1;
-        row[i] = r >= 0 && r < p.rows ? r : -1;
-      }
+      for (int u = 0; u < 4; ++u) row[u] = next[u] >= 0 && next[u] < p.rows ? next[u] : p.rows;
+      if (step + 1 < steps) fetch_ids(step + 1);
       for (int b = 0; b < blocks; ++b, ++t) {
-        if (t >= S && !ptx::mbar_wait(&empty[t % S], (t / S - 1) & 1, abort_flag, kWaitLimitNs)) {
+        if (t >= S && !ptx::mbar_wait_warp(&empty[t % S], (t / S - 1) & 1, abort_flag, kWaitLimitNs)) {
           give_up();
           ok = false;
           break;
         }
-        const uint32_t dst = ptx::smem_u32(smem + t % S * C::STAGE);
-        const int c16 = tid % 16, col = col0 + b * kTile + c16 * 8;
-        const __nv_bfloat16* src = p.X + col;
+        uint8_t* dst = smem + t % S * C::STAGE;
+        const int col = col0 + b * kTile;
+        if (tid == 0) {
+          ptx::mbar_arrive_expect_tx(&full[t % S], C::STAGE + (PROJ && GRAD && step == 0 ? C::RANKS : 0));
+          if constexpr (PROJ && !GRAD) {   // A's columns of this tile
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const bool in = row[i] >= 0 && col < W;
-          cp_async16z(dst + c16 / 8 * kSub + swz(i * 8 + tid / 16, c16 % 8),
-                      in ? src + static_cast<size_t>(row[i]) * W : p.X, in);
-        }
-        if constexpr (PROJ && !GRAD) {  // M = A's columns of this tile
+            for (int h = 0; h < 2; ++h)
+              tma_load_3d(dst + 2 * kSub + h * C::MSUB, &map_m, &full[t % S], col + h * 64, 0, a);
+          }
+          if constexpr (PROJ && GRAD) {    // B's rows of this block, once
+            if (step == 0) {
 #pragma unroll
-          for (int i = 0; i < RP / 8; ++i) {
-            const int j = i * 8 + tid / 16;
-            const bool in = j < R && col < W;
-            cp_async16z(dst + 2 * kSub + c16 / 8 * C::MSUB + swz(j, c16 % 8),
-                        in ? p.M + (static_cast<size_t>(a) * R + j) * W + col : p.M, in);
+              for (int h = 0; h < RP; h += 64)
+                tma_load_3d(s_m + b * C::RANKS + h / 64 * RT::LEAD, &map_m, &full[t % S], h, col, a);
+            }
           }
         }
-        cp_commit();
-        if (t >= LAG) {
-          cp_wait<LAG>();
-          hand_over(t - LAG);
-        }
+        __syncwarp();
+        if (mine)
+          ptx::tma_gather4(dst + sub * kSub + quad * 512, &map_x, &full[t % S], col + sub * 64, row[0], row[1], row[2],
+                           row[3]);
       }
     }
-    cp_wait<0>();
-    if (ok)
-      for (int u = tiles > LAG ? tiles - LAG : 0; u < tiles; ++u) hand_over(u);
-  } else if (warp < 8) {
-    // ---- V in, P out, and at the end G
-    const int et = tid - 128, ew = warp - 4;
-    const uint32_t lane_base = static_cast<uint32_t>(ew * 32) << 16;
+    if (!ok) {   // what is in flight lands before the block ends
+      int never = 0;
+      for (int u = t > S ? t - S : 0; u < t; ++u) ptx::mbar_wait_warp(&full[u % S], (u / S) & 1, &never, kWaitLimitNs);
+    }
+  } else if (warp < kMmaWarp) {
+    // ---- V in, P out, and at the end G.  Two warps to a quarter of TMEM's lanes, half the columns each.
+    const int et = tid - kLoaders, ew = warp - kLoaders / 32, quarter = ew & 3, half = ew >> 2;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const float sc = PROJ && GRAD && p.scale ? __ldg(p.scale + a) : 1.f;
-    auto prepare = [&](int step) {  // rows of V as three terms, rank j's row of 64 of the tile's rows
-      if constexpr (GRAD) {
-        for (int i = et; i < RP * 16; i += 128) {
-          const int j = i % RP, r0 = i / RP * 8;
-          float v[8];
+    constexpr int NP = RP * 16 / kDrainers;   // a thread's pieces of 8 ranks
+    constexpr int HC = RP / 2 > 32 ? 32 : RP / 2;   // TMEM columns read at once
+    int id[NP];
+    float v[NP][8];
+    auto fetch_ids = [&](int step) {  // the rows of V of its pieces
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int at = start + step * kTile + r0 + u;
-            int r = at < end ? (PROJ ? __ldg(p.order + at) : at) : -1;
-            if (PROJ && r >= p.rows) r = -1;
-            v[u] = r >= 0 && j < R ? __ldg(p.V + static_cast<size_t>(r) * R + j) * sc : 0.f;
-          }
-          uint32_t w[kTerms][4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) split3(v[2 * u], v[2 * u + 1], w[0][u], w[1][u], w[2][u]);
-#pragma unroll
-          for (int q = 0; q < kTerms; ++q)
-            *reinterpret_cast<uint4*>(s_v + r0 / 64 * C::V_SUB + swz(q * RP + j, r0 % 64 / 8)) =
-                make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
-        }
-        ptx::fence_proxy_async_smem();
-        ptx::mbar_arrive(&v_full);
+      for (int k = 0; k < NP; ++k) {
+        const int at = start + step * kTile + (et + k * kDrainers) / (RP / 8);
+        id[k] = at < end ? (PROJ ? __ldg(p.order + at) : at) : -1;
+        if (PROJ && id[k] >= p.rows) id[k] = -1;
       }
     };
-    if (want_g) prepare(0);
+    auto fetch_v = [&]() {
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const int j = (et + k * kDrainers) % (RP / 8) * 8;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        if (id[k] >= 0 && j < R) {
+          const float4* from = reinterpret_cast<const float4*>(p.V + static_cast<size_t>(id[k]) * R + j);
+          x = __ldg(from), y = __ldg(from + 1);
+        }
+        v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
+        v[k][4] = y.x, v[k][5] = y.y, v[k][6] = y.z, v[k][7] = y.w;
+      }
+    };
+    auto store_v = [&]() {  // as three terms
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const int i = et + k * kDrainers;
+        const uint32_t at = RT::at(i / (RP / 8), i % (RP / 8));
+        uint32_t w[kTerms][4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) split3(v[k][2 * u] * sc, v[k][2 * u + 1] * sc, w[0][u], w[1][u], w[2][u]);
+#pragma unroll
+        for (int q = 0; q < kTerms; ++q)
+          *reinterpret_cast<uint4*>(s_v + q * C::RANKS + at) = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+      }
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive(&v_full);
+    };
+    if constexpr (GRAD) {
+      if (want_g) {   // past the last step the ids are -1 and nothing is read
+        fetch_ids(0);
+        fetch_v();
+        fetch_ids(1);
+        store_v();
+        fetch_v();
+        fetch_ids(2);
+      }
+    }
     bool ok = true;
     for (int step = 0; step < (GRAD ? steps : 0); ++step) {
       // the step's MMAs are done: V may be replaced, P is complete
@@ -246,26 +283,33 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<RP, PROJ, GRAD>::PER
         ok = false;
         break;
       }
-      if (want_g && step + 1 < steps) prepare(step + 1);
+      if constexpr (GRAD) {
+        if (want_g && step + 1 < steps) {
+          store_v();
+          fetch_v();
+          fetch_ids(step + 3);
+        }
+      }
       if constexpr (PROJ) {
         if (want_p) {
           ptx::tc_fence_after();
-          const int at = start + step * kTile + ew * 32 + lane;
+          const int at = start + step * kTile + quarter * 32 + lane;
           float* o = p.proj + (static_cast<size_t>(slice) * p.rows + at) * R;
           const uint32_t from = tmem + lane_base + C::PCOL + step % C::PBUF * RP;
 #pragma unroll
-          for (int j = 0; j < RP; j += 16) {
-            uint32_t r[16];
+          for (int u = 0; u < RP / 2; u += HC) {
+            uint32_t r[HC];
             __syncwarp();
-            ptx::tmem_ld_32x32b_x16(from + j, r);
+            tmem_ld(from + half * (RP / 2) + u, r);
             ptx::tmem_ld_wait();
-            if (at < end) {
 #pragma unroll
-              for (int u = 0; u < 16; u += 4)
-                if (j + u < R)
-                  *reinterpret_cast<float4*>(o + j + u) =
-                      make_float4(__uint_as_float(r[u]) * sc, __uint_as_float(r[u + 1]) * sc,
-                                  __uint_as_float(r[u + 2]) * sc, __uint_as_float(r[u + 3]) * sc);
+            for (int e = 0; e < HC; e += 8) {
+              const int j = half * (RP / 2) + u + e;
+              if (at >= end || j >= R) continue;
+              float x[8];
+#pragma unroll
+              for (int q = 0; q < 8; ++q) x[q] = __uint_as_float(r[e + q]) * sc;
+              store32(o + j, x);
             }
           }
           ptx::tc_fence_before();
@@ -274,19 +318,19 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<RP, PROJ, GRAD>::PER
       }
     }
     if constexpr (!GRAD) {   // the slice's P to shared memory, over the stages: their MMAs are done
-      float* s_p = reinterpret_cast<float*>(smem) + et * C::PS;
+      float* s_p = reinterpret_cast<float*>(smem) + (quarter * 32 + lane) * C::PS + half * (RP / 2);
       if (blocks == 0) {
-        for (int j = 0; j < RP; j += 4) *reinterpret_cast<float4*>(s_p + j) = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < RP / 2; j += 4) *reinterpret_cast<float4*>(s_p + j) = make_float4(0.f, 0.f, 0.f, 0.f);
       } else if (ptx::mbar_wait_warp(&step_done[0], 0, abort_flag, kWaitLimitNs)) {
         ptx::tc_fence_after();
 #pragma unroll
-        for (int j = 0; j < RP; j += 16) {
-          uint32_t r[16];
+        for (int j = 0; j < RP / 2; j += 8) {
+          uint32_t r[8];
           __syncwarp();
-          ptx::tmem_ld_32x32b_x16(tmem + lane_base + j, r);
+          ptx::tmem_ld_32x32b_x8(tmem + lane_base + half * (RP / 2) + j, r);
           ptx::tmem_ld_wait();
 #pragma unroll
-          for (int u = 0; u < 16; u += 4)
+          for (int u = 0; u < 8; u += 4)
             *reinterpret_cast<uint4*>(s_p + j + u) = make_uint4(r[u], r[u + 1], r[u + 2], r[u + 3]);
         }
       } else {
@@ -302,35 +346,44 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<RP, PROJ, GRAD>::PER
         float* part = p.part + static_cast<size_t>(slot) * size;
         float* g32 = static_cast<float*>(p.grad) + a * size;
         __nv_bfloat16* g16 = static_cast<__nv_bfloat16*>(p.grad) + a * size;
+        // [W][R]: through shared memory (over the stages and B: the MMAs are done), where a thread holds a
+        // column's ranks, out in whole rows; [R][W]: neighbouring lanes hold neighbouring columns already
+        float* s_g = reinterpret_cast<float*>(smem) + ew * 32 * C::GS;
         for (int b = 0; b < blocks; ++b) {
-          const int k = col0 + b * kTile + ew * 32 + lane;
+          const int k0 = col0 + b * kTile + quarter * 32, k = k0 + lane;
 #pragma unroll
-          for (int j = 0; j < RP; j += 16) {
-            float v[16];
+          for (int u = 0; u < RP / 2; u += HC) {
+            float x[HC];
             __syncwarp();
-            load_grad16<C::STACK, RP>(tmem + lane_base + b * C::GCOLS + j, v);
-            if (k >= W) {
-            } else if constexpr (PROJ) {  // [W][R]: a column's ranks side by side
-              const size_t o = static_cast<size_t>(k) * R + j;
+            load_grad<C::STACK, RP>(tmem + lane_base + b * C::GCOLS + half * (RP / 2) + u, x);
+            if constexpr (PROJ) {
 #pragma unroll
-              for (int u = 0; u < 16; u += 8) {
-                if (j + u >= R) continue;
-                float x[8];
+              for (int q = 0; q < HC; q += 4)
+                *reinterpret_cast<float4*>(s_g + lane * C::GS + u + q) = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
+            } else {
 #pragma unroll
-                for (int q = 0; q < 8; ++q) x[q] = v[u + q];
-                if (!whole) store8(part + o + u, x);
-                else if (p.grad_f32) store8(g32 + o + u, x);
-                else store8(g16 + o + u, x);
+              for (int q = 0; q < HC; ++q) {
+                const int j = half * (RP / 2) + u + q;
+                const size_t o = static_cast<size_t>(j) * W + k;
+                if (k >= W || j >= R) continue;
+                if (!whole) part[o] = x[q];
+                else if (p.grad_f32) g32[o] = x[q];
+                else g16[o] = __float2bfloat16_rn(x[q]);
               }
-            } else {                      // [R][W]
+            }
+          }
+          if constexpr (PROJ) {
+            constexpr int PC = RP / 8;     // pieces of 4 ranks in half a row
+            __syncwarp();
 #pragma unroll
-              for (int u = 0; u < 16; ++u) {
-                if (j + u >= R) continue;
-                const size_t o = static_cast<size_t>(j + u) * W + k;
-                if (!whole) part[o] = v[u];
-                else if (p.grad_f32) g32[o] = v[u];
-                else g16[o] = __float2bfloat16_rn(v[u]);
-              }
+            for (int i = 0; i < PC; ++i) {
+              const int m = i * (32 / PC) + lane / PC, j = lane % PC * 4, rank = half * (RP / 2) + j;
+              const float4 x = *reinterpret_cast<const float4*>(s_g + m * C::GS + j);
+              if (k0 + m >= W || rank >= R) continue;
+              const size_t o = static_cast<size_t>(k0 + m) * R + rank;
+              if (!whole) *reinterpret_cast<float4*>(part + o) = x;
+              else if (p.grad_f32) *reinterpret_cast<float4*>(g32 + o) = x;
+              else *reinterpret_cast<uint2*>(g16 + o) = make_uint2(pack2(x.x, x.y), pack2(x.z, x.w));
             }
           }
         }
@@ -339,8 +392,8 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<RP, PROJ, GRAD>::PER
     ptx::tc_fence_before();
   } else if (lane == 0) {
     // ---- MMAs
-    constexpr uint32_t IP = ptx::make_idesc(128, RP, 1);
-    constexpr uint32_t IG = ptx::make_idesc(128, C::STACK ? kTerms * RP : RP, 1) | kAMn;
+    constexpr uint32_t IP = ptx::make_idesc(128, RP, 1) | (GRAD ? kBMn : 0u);
+    constexpr uint32_t IG = ptx::make_idesc(128, C::STACK ? kTerms * RP : RP, 1) | kAMn | kBMn;
     bool ok = true;
     int t = 0;
     for (int step = 0; step < steps && blocks > 0 && ok; ++step) {
@@ -353,12 +406,14 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<RP, PROJ, GRAD>::PER
         ptx::tc_fence_after();
         const uint32_t x = ptx::smem_u32(smem + t % S * C::STAGE);
         if (want_p) {
-          const uint32_t m = PROJ && !GRAD ? x + 2 * kSub : ptx::smem_u32(s_m) + b * 2 * C::MSUB;
           const uint32_t d = tmem + C::PCOL + step % C::PBUF * RP;
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            ptx::umma_f16(d, ptx::sw128_kmajor_desc(x + k / 4 * kSub) + k % 4 * 2,
-                          ptx::sw128_kmajor_desc(m + k / 4 * C::MSUB) + k % 4 * 2, IP, b > 0 || k > 0);
+          for (int k = 0; k < 8; ++k) {  // 16 columns at a time
+            const uint64_t md =
+                GRAD ? RT::desc(ptx::smem_u32(s_m) + b * C::RANKS + k * 16 * RT::ROW, RT::LEAD)
+                     : ptx::sw128_kmajor_desc(x + 2 * kSub + k / 4 * C::MSUB) + k % 4 * 2;
+            ptx::umma_f16(d, ptx::sw128_kmajor_desc(x + k / 4 * kSub) + k % 4 * 2, md, IP, b > 0 || k > 0);
+          }
         }
         if (want_g) {
           const uint32_t v = ptx::smem_u32(s_v);
@@ -366,13 +421,13 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<RP, PROJ, GRAD>::PER
 #pragma unroll
           for (int k = 0; k < 8; ++k) {  // 16 rows at a time
             const uint64_t xd = mn_desc(x + k * 2048, kSub);
-            const uint64_t vd = ptx::sw128_kmajor_desc(v + k / 4 * C::V_SUB) + k % 4 * 2;
-            if constexpr (C::STACK) {
-              ptx::umma_f16(d, xd, vd, IG, step > 0 || k > 0);
+            if constexpr (C::STACK) {    // the terms side by side: each a unit of the layout
+              ptx::umma_f16(d, xd, RT::desc(v + k * 16 * RT::ROW, C::RANKS), IG, step > 0 || k > 0);
             } else {
 #pragma unroll
               for (int q = 0; q < kTerms; ++q)
-                ptx::umma_f16(d, xd, vd + (q * RP * 128 >> 4), IG, step > 0 || k > 0 || q > 0);
+                ptx::umma_f16(d, xd, RT::desc(v + q * C::RANKS + k * 16 * RT::ROW, RT::LEAD), IG,
+                              step > 0 || k > 0 || q > 0);
             }
           }
         }
@@ -389,7 +444,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<RP, PROJ, GRAD>::PER
   }
   __syncwarp();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kMmaWarp) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, C::TMEM);
   }
@@ -398,7 +453,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamCfg<RP, PROJ, GRAD>::PER
     __syncwarp();
     cluster_arrive();
     cluster_wait();
-    for (int i = tid; i < kTile / static_cast<int>(CS) * (RP / 4); i += kStreamThreads) {
+    for (int i = tid; i < kTile / static_cast<int>(CS) * (RP / 4); i += C::THREADS) {
       const int m = i / (RP / 4) * static_cast<int>(CS) + slice, j = i % (RP / 4) * 4;
       if (start + m >= end || j >= R) continue;
       const float4* from = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem) + m * C::PS + j);
@@ -424,11 +479,17 @@ int launch_stream(const StreamArgs& p, cudaStream_t s) {
   auto kernel = lora_stream_kernel<RP, PROJ, GRAD>;
   const int st = allow_smem(done, kernel, C::SMEM);
   if (st != MOE_OK) return st;
+  CUtensorMap mx, mm;
+  if (!make_map(&mx, p.X, 2, p.rows, p.W, 1)) return MOE_ERR_CUDA;
+  mm = mx;
+  if (PROJ && !GRAD && !make_adapter_map(&mm, p.M, p.n, p.R, p.W, RP, 64)) return MOE_ERR_CUDA;
+  if (PROJ && GRAD && !make_adapter_map(&mm, p.M, p.n, p.W, p.R, kTile, RP < 64 ? RP : 64)) return MOE_ERR_CUDA;
   const unsigned slots = static_cast<unsigned>(p.rows / p.chunk + p.n), slices = (p.W + p.cols - 1) / p.cols;
   if constexpr (!GRAD)
-    return launch_cluster("lora_stream_kernel", kernel, dim3(slots * p.cluster), dim3(kStreamThreads), C::SMEM, p.cluster, s, p);
+    return launch_cluster("lora_stream_kernel", kernel, dim3(slots * p.cluster), dim3(C::THREADS), C::SMEM, p.cluster, s,
+                          p, mx, mm);
   else
-    return launch_pdl("lora_stream_kernel", kernel, dim3(slots, slices), dim3(kStreamThreads), C::SMEM, s, p);
+    return launch_pdl("lora_stream_kernel", kernel, dim3(slots, slices), dim3(C::THREADS), C::SMEM, s, p, mx, mm);
 }
 template <bool PROJ, bool GRAD>
 int launch_stream_rank(const StreamArgs& p, cudaStream_t s) {
@@ -439,6 +500,29 @@ int launch_stream_rank(const StreamArgs& p, cudaStream_t s) {
 }
 
 }  // namespace
+
+bool make_adapter_map(CUtensorMap* m, const void* base, uint64_t n, uint64_t rows, uint64_t cols, uint32_t box_rows,
+                      uint32_t box_cols) {
+  const EncodeTiledFn enc = get_encode_fn();
+  if (!enc) {
+    record_cuda_error(cudaErrorNotSupported, "cuTensorMapEncodeTiled unavailable from the driver");
+    return false;
+  }
+  const cuuint64_t dims[3] = {cols, rows, n};
+  const cuuint64_t strides[2] = {cols * 2, rows * cols * 2};
+  const cuuint32_t box[3] = {box_cols, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapSwizzle swizzle = box_cols == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                     : box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                      : CU_TENSOR_MAP_SWIZZLE_32B;
+  if (enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
+    record_cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled rejected the adapters' layout");
+    return false;
+  }
+  return true;
+}
 
 int lora_stream_max_cols(int R) {
   return kTile * (R <= 16   ? StreamCfg<16, true, true>::BLOCKS
