@@ -410,27 +410,27 @@ int launch_adapter_plan(const int32_t* adapter, int rows, int n, int32_t* offset
 bool lora_two_launches(int rows, int n) { return rows > 16ll * n; }
 
 size_t lora_workspace_bytes(int rows, int n, int R) {
-  return lora_two_launches(rows, n) ? 256 + static_cast<size_t>(rows) * R * 4 : 0;
+  return lora_two_launches(rows, n) ? 256 + image_bytes(rows, n, R) : 0;
 }
 
 int launch_lora(const LoraForwardArgs& q, cudaStream_t s) {
   if (q.rows == 0) return MOE_OK;
   if (lora_two_launches(q.rows, q.n)) {
     int* status = static_cast<int*>(q.ws);
-    float* h = reinterpret_cast<float*>(static_cast<char*>(q.ws) + 256);
+    uint8_t* h = static_cast<uint8_t*>(q.ws) + 256;
     StreamArgs p{};
     p.X = static_cast<const __nv_bfloat16*>(q.x), p.M = static_cast<const __nv_bfloat16*>(q.A);
     p.offsets = q.offsets, p.order = q.order, p.n = q.n, p.rows = q.rows, p.W = q.d, p.R = q.R;
-    p.proj = h, p.h_out = q.h_out, p.status = status;
+    p.scale = q.scale, p.image = h, p.h_out = q.h_out, p.status = status;
     // slices of a row: as many as leave two CTAs to an SM, up to the portable cluster
-    const long long tiles = static_cast<long long>(q.rows) / 128 + q.n;
+    const long long tiles = (static_cast<long long>(q.rows) + 64ll * q.n) / 128 + 1;  // an adapter's last is half full
     p.chunk = 128, p.cluster = 1;
     while (p.cluster < 8 && tiles * p.cluster <= num_sms() && q.d > p.cluster * 128) p.cluster *= 2;
     p.cols = ((q.d + p.cluster - 1) / p.cluster + 127) / 128 * 128;
     const int st = launch_lora_stream(p, kStreamProject, s);
     if (st != MOE_OK) return st;
     ExpandArgs e{};
-    e.h = h, e.M = static_cast<const __nv_bfloat16*>(q.B), e.scale = q.scale, e.offsets = q.offsets, e.order = q.order;
+    e.h = h, e.M = static_cast<const __nv_bfloat16*>(q.B), e.offsets = q.offsets, e.order = q.order;
     e.n = q.n, e.rows = q.rows, e.N = q.N, e.R = q.R, e.base = q.base, e.out = q.out, e.h_out = q.h_out;
     e.status = status;
     return launch_lora_expand(e, false, q.out_dtype, s);

@@ -14,26 +14,79 @@
 namespace moe {
 namespace {
 
-// dh = the slices' sum, for the rows that have an adapter
-__global__ void __launch_bounds__(256) dh_reduce_kernel(const float* __restrict__ part, const int32_t* __restrict__ off,
-                                                        int n, int rows, int R, int slices, float* __restrict__ dh) {
+// The images of a tile's 128 rows, blockIdx.y's share of them: of s h, whose rows
+// are the plan's (SLICES false), or of dh, the sum of its slices by position.
+// Rows behind an adapter's last are 0: a gradient sums over all 128.
+struct TermsArgs {
+  const float* h;
+  int slices;
+  const float* scale;
+  const int32_t* offsets;
+  const int32_t* order;
+  int n, rows, R;
+  uint8_t* image;
+};
+// A piece of 8 ranks is a thread's, or, of many slices, kGroups threads' (the
+// lanes 8 apart), each with every kGroups-th slice; they meet by shuffles.
+constexpr int kTermsThreads = 256, kGroups = 4;
+
+template <int RP, bool SLICES>
+__global__ void __launch_bounds__(kTermsThreads) lora_terms_kernel(const TermsArgs p) {
+  constexpr int G = SLICES ? kGroups : 1, PIECES = RP / 8, ROWS = kTermsThreads / G / PIECES;   // rows of a block
   pdl_wait();
   pdl_launch_dependents();
-  const size_t all = static_cast<size_t>(rows) * R, used = static_cast<size_t>(held_offset(off, n, rows, n)) * R;
-  for (size_t i = (static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x) * 4; i < used;
-       i += static_cast<size_t>(gridDim.x) * blockDim.x * 4) {
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int s = 0; s < slices; ++s) {
-      const float4 u = __ldg(reinterpret_cast<const float4*>(part + s * all + i));
-      v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+  int a, start, end;
+  if (!find_tile(p.offsets, p.n, p.rows, 128, blockIdx.x, a, start, end) || a == p.n) return;
+  const int g = SLICES ? threadIdx.x / 8 % G : 0, i = SLICES ? threadIdx.x / 32 * 8 + threadIdx.x % 8 : threadIdx.x;
+  const int c = i % PIECES, m = blockIdx.y * ROWS + i / PIECES, at = start + m;
+  if (m >= 128) return;   // whole warps: 128 rows fill the last block or half of one
+  float v[8] = {};
+  if (at < end && c * 8 < p.R) {
+    if constexpr (SLICES) {
+      const size_t all = static_cast<size_t>(p.rows) * p.R;
+      const float* from = p.h + static_cast<size_t>(at) * p.R + c * 8;
+#pragma unroll 8
+      for (int s = g; s < p.slices; s += G) {
+        float u[8];
+        load8(from + s * all, u);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] += u[q];
+      }
+    } else {
+      const int r = __ldg(p.order + at);
+      const float sc = p.scale ? __ldg(p.scale + a) : 1.f;
+      if (r >= 0 && r < p.rows) load8(p.h + static_cast<size_t>(r) * p.R + c * 8, v);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] *= sc;
     }
-    *reinterpret_cast<float4*>(dh + i) = v;
   }
+  if constexpr (SLICES) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      v[q] += __shfl_xor_sync(0xffffffffu, v[q], 8);
+      v[q] += __shfl_xor_sync(0xffffffffu, v[q], 16);
+    }
+    if (g) return;
+  }
+  store_terms<RP>(p.image + static_cast<size_t>(blockIdx.x) * RankTile<RP>::IMAGE, m, c, v);
+}
+
+template <int RP, bool SLICES>
+int launch_terms_rank(const TermsArgs& p, cudaStream_t s) {
+  constexpr int rows = kTermsThreads / (SLICES ? kGroups : 1) / (RP / 8);
+  return launch_pdl("lora_terms_kernel", lora_terms_kernel<RP, SLICES>, dim3(p.rows / 128 + p.n, (128 + rows - 1) / rows),
+                    dim3(kTermsThreads), 0, s, p);
+}
+template <bool SLICES>
+int launch_terms(const TermsArgs& p, cudaStream_t s) {
+  if (p.R <= 16) return launch_terms_rank<16, SLICES>(p, s);
+  if (p.R <= 32) return launch_terms_rank<32, SLICES>(p, s);
+  if (p.R <= 64) return launch_terms_rank<64, SLICES>(p, s);
+  return launch_terms_rank<128, SLICES>(p, s);
 }
 
 struct GradReduceArgs {
-  const float* part[2];   // of dA, dB: partial sums by chunk slot
+  const float* part[2];   // of dA, dB: partial sums by part_slot
   void* grad[2];          // nullptr: not wanted
   size_t size[2];         // values of one adapter
   int chunk[2];
@@ -42,7 +95,7 @@ struct GradReduceArgs {
 };
 
 // Adapter blockIdx.y's gradient blockIdx.z (0 dA, 1 dB): the sum over its
-// chunks, 0 where it has no rows.  That of a single chunk is there already.
+// chunks.  That of a single one, or of none, is there already.
 template <typename GT>
 __global__ void __launch_bounds__(256) grad_reduce_kernel(const GradReduceArgs p) {
   pdl_wait();
@@ -50,9 +103,9 @@ __global__ void __launch_bounds__(256) grad_reduce_kernel(const GradReduceArgs p
   const int a = blockIdx.y, z = blockIdx.z, chunk = p.chunk[z];
   const int b = held_offset(p.offsets, p.n, p.rows, a), e = held_offset(p.offsets, p.n, p.rows, a + 1);
   const int chunks = e > b ? (e - b + chunk - 1) / chunk : 0;
-  if (chunks == 1 || !p.grad[z]) return;
+  if (chunks <= 1 || !p.grad[z]) return;
   const size_t size = p.size[z];
-  const float* part = p.part[z] + static_cast<size_t>(b / chunk + a) * size;
+  const float* part = p.part[z] + part_slot(b, chunk) * size;
   GT* grad = static_cast<GT*>(p.grad[z]) + a * size;
   for (size_t i = (static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x) * 4; i < size;
        i += static_cast<size_t>(gridDim.x) * blockDim.x * 4) {
@@ -69,30 +122,34 @@ __global__ void __launch_bounds__(256) grad_reduce_kernel(const GradReduceArgs p
   }
 }
 
-// Rows and columns of a CTA of a pass over [rows, W].  An estimate of its time
-// from the traffic: the tiles of the busiest SM, each CTA's start and end, and
-// the partial sums, which several chunks of an adapter (dA, dB) and several
-// slices of a row (dh) write and read again.  How the rows are spread over the
-// adapters is on the device; an even spread is taken.
+// Rows and columns of a CTA of a pass over [rows, W], from an estimate of its
+// time: a CTA's tiles at its share of the memory's rate, its start (3 us to the
+// first product) and its gradient's way out, over as many as an SM holds; the
+// partial sums, which several chunks of an adapter (dA, dB) and several slices
+// of a row (dh) write and read again; the launch that adds them.  How the rows
+// are spread over the adapters is on the device: some are taken to have twice
+// their even share, the longest CTA to run on for half its time.
 struct Split {
   int chunk, cols;
 };
 Split split_for(int rows, int n, int W, int R, bool proj) {
-  const int max_cols = lora_stream_max_cols(R), per_sm = R <= 32 ? 2 : 1;
-  const double ns_per_byte = 148.0 / 6400.0, per_adapter = static_cast<double>(rows) / n;
+  const int max_cols = lora_stream_max_cols(R, proj), per_sm = R <= 32 ? 2 : 1, sms = num_sms();
+  const double rate = 6400.0, mean = static_cast<double>(rows) / (n < rows ? n : rows > 0 ? rows : 1);
   Split best{128, 128};
   double best_ns = 1e30;
   for (int cols = 128; cols <= max_cols; cols *= 2)
-    for (int chunk = 128; chunk <= 4096; chunk *= 2) {
-      const double each = per_adapter < chunk ? 1.0 : per_adapter / chunk + 0.5;
-      const double ctas = n * each * ((W + cols - 1) / cols);
-      const double waves = ctas / (num_sms() * per_sm) < 1.0 ? 1.0 : ctas / (num_sms() * per_sm) + 0.5;
-      const double tile = 128.0 * 128 * 2 * ns_per_byte * per_sm;
-      const double used = per_adapter < chunk ? per_adapter : chunk;
-      const double cta = (used + 127) / 128 * (cols / 128) * tile + 4000;
-      double partial = each > 1.0 ? 8.0 * n * each * W * R : 0.0;
-      if (proj) partial += 8.0 * rows * R * ((W + cols - 1) / cols);
-      const double ns = waves * cta + partial * ns_per_byte / num_sms() * 0.7;
+    for (int chunk = 128; chunk <= 8192; chunk *= 2) {
+      const int slices = (W + cols - 1) / cols;
+      const bool whole = chunk >= (n > 1 ? 2 : 1) * mean;
+      const double chunks = whole ? rows / mean : rows / mean * 0.5 + static_cast<double>(rows) / chunk;
+      const double ctas = chunks * slices, load = ctas / (sms * per_sm);
+      const double tile = 128.0 * 128 * 2 * sms / rate * (ctas > sms ? per_sm : 1);
+      const double longest = mean * (n > 1 ? 2 : 1) < chunk ? mean * (n > 1 ? 2 : 1) : chunk;
+      const double fixed = 3000 + cols * R * 4 * sms / rate;
+      const double ns = load * fixed + (load < 1 ? 1 - load : 0.5) * (fixed + (longest + 127) / 128 * (cols / 128) * tile) +
+                        static_cast<double>(rows) / 128 * slices * (cols / 128) * tile / (sms * per_sm) +
+                        ((whole ? 0.0 : 8.0 * chunks * W * R) + (proj ? 8.0 * rows * R * slices : 0.0)) / rate +
+                        (rows > chunk ? 3000 : 0);
       if (ns < best_ns) best_ns = ns, best = {chunk, cols};
     }
   return best;
@@ -100,7 +157,7 @@ Split split_for(int rows, int n, int W, int R, bool proj) {
 
 struct BackwardLayout {
   Split dc, x;
-  size_t dh_part, dh, pA, pB, total;
+  size_t dh_part, image, pA, pB, total;
 };
 BackwardLayout backward_layout(int rows, int n, int d, int N, int R) {
   BackwardLayout L{};
@@ -114,9 +171,9 @@ BackwardLayout backward_layout(int rows, int n, int d, int N, int R) {
   L.x = split_for(rows, n, d, R, false);
   const size_t slices = (N + L.dc.cols - 1) / L.dc.cols;
   L.dh_part = take(slices * rows * R * 4);
-  L.dh = take(static_cast<size_t>(rows) * R * 4);
-  L.pA = take((static_cast<size_t>(rows) / L.x.chunk + n) * R * d * 4);
-  L.pB = take((static_cast<size_t>(rows) / L.dc.chunk + n) * R * N * 4);
+  L.image = take(image_bytes(rows, n, R));   // of h, then of dh
+  L.pA = take(part_slot(rows, L.x.chunk) * R * d * 4);
+  L.pB = take(part_slot(rows, L.dc.chunk) * R * N * 4);
   L.total = off;
   return L;
 }
@@ -131,51 +188,60 @@ int launch_lora_backward(const LoraBackwardArgs& q, cudaStream_t s) {
   const BackwardLayout L = backward_layout(q.rows, q.n, q.d, q.N, q.R);
   char* ws = static_cast<char*>(q.ws);
   float* dh_part = reinterpret_cast<float*>(ws + L.dh_part);
-  float* dh = reinterpret_cast<float*>(ws + L.dh);
-  const bool need_dh = q.dx || q.dA;
+  uint8_t* image = reinterpret_cast<uint8_t*>(ws + L.image);
+  const size_t sizeA = static_cast<size_t>(q.R) * q.d, sizeB = static_cast<size_t>(q.R) * q.N;
   if (q.rows == 0) {
     MOE_CUDA_CHECK(cudaMemsetAsync(ws, 0, sizeof(int), s));   // MOE_OK
-  } else {
-    StreamArgs p{};
-    p.X = static_cast<const __nv_bfloat16*>(q.dC), p.M = static_cast<const __nv_bfloat16*>(q.B), p.V = q.h;
-    p.scale = q.scale, p.offsets = q.offsets, p.order = q.order, p.n = q.n, p.rows = q.rows, p.W = q.N, p.R = q.R;
-    p.chunk = L.dc.chunk, p.cols = L.dc.cols;
-    p.proj = need_dh ? dh_part : nullptr;
-    p.part = reinterpret_cast<float*>(ws + L.pB), p.grad = q.dB, p.grad_f32 = q.grad_dtype == MOE_F32;
-    p.status = reinterpret_cast<int*>(ws);
-    int st = launch_lora_stream(p, kStreamBoth, s);
-    if (st != MOE_OK) return st;
-    const int slices = (q.N + L.dc.cols - 1) / L.dc.cols;
-    if (need_dh && slices > 1) {
-      const size_t quads = static_cast<size_t>(q.rows) * q.R / 4;
-      const unsigned grid = static_cast<unsigned>(quads / 256 + 1 < 1184 ? quads / 256 + 1 : 1184);
-      st = launch_pdl("dh_reduce_kernel", dh_reduce_kernel, dim3(grid), dim3(256), 0, s,
-                      static_cast<const float*>(dh_part), q.offsets, q.n, q.rows, q.R, slices, dh);
-      if (st != MOE_OK) return st;
-    } else {
-      dh = dh_part;
-    }
-    if (q.dA) {
-      p.X = static_cast<const __nv_bfloat16*>(q.x), p.M = nullptr, p.V = dh, p.scale = nullptr, p.W = q.d;
-      p.chunk = L.x.chunk, p.cols = L.x.cols, p.proj = nullptr;
-      p.part = reinterpret_cast<float*>(ws + L.pA), p.grad = q.dA;
-      st = launch_lora_stream(p, kStreamGrad, s);
-      if (st != MOE_OK) return st;
-    }
-    if (q.dx) {
-      ExpandArgs e{};
-      e.h = dh, e.M = static_cast<const __nv_bfloat16*>(q.A), e.offsets = q.offsets, e.order = q.order;
-      e.n = q.n, e.rows = q.rows, e.N = q.d, e.R = q.R, e.base = q.dx_base, e.out = q.dx;
-      e.status = reinterpret_cast<int*>(ws);
-      st = launch_lora_expand(e, true, q.dx_dtype, s);
-      if (st != MOE_OK) return st;
-    }
+    const size_t bytes = q.grad_dtype == MOE_F32 ? 4 : 2;
+    if (q.dA) MOE_CUDA_CHECK(cudaMemsetAsync(q.dA, 0, q.n * sizeA * bytes, s));
+    if (q.dB) MOE_CUDA_CHECK(cudaMemsetAsync(q.dB, 0, q.n * sizeB * bytes, s));
+    return MOE_OK;
   }
-  if (!q.dA && !q.dB) return MOE_OK;
+  const bool need_dh = q.dx || q.dA;
+  TermsArgs t{};
+  t.scale = q.scale, t.offsets = q.offsets, t.order = q.order, t.n = q.n, t.rows = q.rows, t.R = q.R, t.image = image;
+  int st = MOE_OK;
+  if (q.dB) {
+    t.h = q.h;
+    st = launch_terms<false>(t, s);
+    if (st != MOE_OK) return st;
+  }
+  StreamArgs p{};
+  p.X = static_cast<const __nv_bfloat16*>(q.dC), p.M = static_cast<const __nv_bfloat16*>(q.B), p.V = image;
+  p.scale = q.scale, p.offsets = q.offsets, p.order = q.order, p.n = q.n, p.rows = q.rows, p.W = q.N, p.R = q.R;
+  p.chunk = L.dc.chunk, p.cols = L.dc.cols;
+  p.proj = need_dh ? dh_part : nullptr;
+  p.part = reinterpret_cast<float*>(ws + L.pB), p.grad = q.dB, p.grad_f32 = q.grad_dtype == MOE_F32;
+  p.status = reinterpret_cast<int*>(ws);
+  st = launch_lora_stream(p, kStreamBoth, s);
+  if (st != MOE_OK) return st;
+  if (need_dh) {
+    t.h = dh_part, t.slices = (q.N + L.dc.cols - 1) / L.dc.cols;
+    st = launch_terms<true>(t, s);
+    if (st != MOE_OK) return st;
+  }
+  if (q.dA) {
+    p.X = static_cast<const __nv_bfloat16*>(q.x), p.M = nullptr, p.W = q.d;
+    p.chunk = L.x.chunk, p.cols = L.x.cols, p.proj = nullptr;
+    p.part = reinterpret_cast<float*>(ws + L.pA), p.grad = q.dA;
+    st = launch_lora_stream(p, kStreamGrad, s);
+    if (st != MOE_OK) return st;
+  }
+  if (q.dx) {
+    ExpandArgs e{};
+    e.h = image, e.M = static_cast<const __nv_bfloat16*>(q.A), e.offsets = q.offsets, e.order = q.order;
+    e.n = q.n, e.rows = q.rows, e.N = q.d, e.R = q.R, e.base = q.dx_base, e.out = q.dx;
+    e.status = reinterpret_cast<int*>(ws);
+    st = launch_lora_expand(e, true, q.dx_dtype, s);
+    if (st != MOE_OK) return st;
+  }
+  // an adapter of several chunks has to have more rows than one holds
+  const bool manyA = q.dA && q.rows > L.x.chunk, manyB = q.dB && q.rows > L.dc.chunk;
+  if (!manyA && !manyB) return MOE_OK;
   GradReduceArgs r{};
   r.part[0] = reinterpret_cast<float*>(ws + L.pA), r.part[1] = reinterpret_cast<float*>(ws + L.pB);
-  r.grad[0] = q.dA, r.grad[1] = q.dB;
-  r.size[0] = static_cast<size_t>(q.R) * q.d, r.size[1] = static_cast<size_t>(q.R) * q.N;
+  r.grad[0] = manyA ? q.dA : nullptr, r.grad[1] = manyB ? q.dB : nullptr;
+  r.size[0] = sizeA, r.size[1] = sizeB;
   r.chunk[0] = L.x.chunk, r.chunk[1] = L.dc.chunk;
   r.offsets = q.offsets, r.n = q.n, r.rows = q.rows;
   // eight blocks to an SM over all the adapters, no more than one pass needs

@@ -11,9 +11,10 @@
 // from there, where 8 neighbouring lanes hold one: full 128-byte lines both
 // ways although the rows lie scattered.
 //
-// h enters as two bf16 terms (hi + lo, 2^-17 of it left out) for a bf16 result
-// and as three (all of an fp32 value) for an fp32 one: one term's rounding
-// would stand beside the result's own.
+// h comes split and laid out (lora_tc.cuh), scale and all, by one bulk copy: as
+// two bf16 terms (2^-17 of it left out) for a bf16 result and as three (all of
+// an fp32 value) for an fp32 one.  One term's rounding would stand beside the
+// result's own.
 //
 // Waits are limited and abort as in the streaming pass.
 #include <cstdint>
@@ -34,8 +35,7 @@ constexpr int kBC = 64;  // columns of a block
 template <int RP, bool KN, typename OT>
 struct ExpandCfg {
   static constexpr int TERMS = sizeof(OT) == 4 ? 3 : 2;
-  static constexpr int HSUBS = (TERMS * RP + 63) / 64;
-  static constexpr int H = HSUBS * kRows * 128;                    // h's terms, [128][64] tiles
+  static constexpr int H = TERMS * RankTile<RP>::BYTES;            // h's terms
   static constexpr int BASE = kRows * kBC * sizeof(OT);
   static constexpr int WBYTES = KN ? RP * 128 : (RP + 63) / 64 * kBC * 128;
   static constexpr int STAGE = BASE + WBYTES;
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
       ptx::mbar_init(&acc_full[i], 1);
       ptx::mbar_init(&acc_free[i], kDrainers);
     }
-    ptx::mbar_init(&h_full, kDrainers);
+    ptx::mbar_init(&h_full, 1);
     ptx::mbar_init(&drained, 1);
     s_abort = 0;
     ptx::fence_mbar_init();
@@ -109,20 +109,9 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
   }
   const int blocks = (col1 - col0 + kBC - 1) / kBC;
 
-  const int et = tid - kLoaders;
-  constexpr int NP = RP * 16 / kDrainers;   // a drainer's pieces of 8 ranks of h
-  float v[NP][8];
   if (warp == kMmaWarp) {
     ptx::tmem_alloc(&s_tmem, 2 * kBC);
     ptx::tmem_relinquish();
-  } else if (et >= 0) {                     // h's loads are in flight across the setup
-#pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      const int i = et + k * kDrainers, m = i / (RP / 8), j = i % (RP / 8) * 8;
-#pragma unroll
-      for (int u = 0; u < 8; ++u) v[k][u] = 0.f;
-      if (start + m < end && j < R) load8(p.h + static_cast<size_t>(start + m) * R + j, v[k]);
-    }
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -137,7 +126,12 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
     // ---- base tiles and the adapter's columns.  Lane l of a warp gathers its (l % 8)-th four rows, the
     // (l / 8)-th 128 bytes of the block; a row that is not there is taken from behind base, as zeros.
     constexpr int SUBS = kBC * sizeof(OT) / 128;
-    const int quad = warp * 8 + lane % 8, sub = lane / 8;
+    const int quad = warp * 8 + lane % 8, sub = lane / 8, quads = (end - start + 3) / 4;  // none behind the last row
+    if (tid == 0) {
+      ptx::mbar_arrive_expect_tx(&h_full, C::H);
+      bulk_load(s_h, p.h + static_cast<size_t>(blockIdx.x) * RankTile<RP>::IMAGE, C::H, &h_full);
+    }
+    const uint64_t policy = ptx::policy_evict_first();
     int row[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) row[u] = s_row[quad * 4 + u] >= 0 ? s_row[quad * 4 + u] : p.rows;
@@ -152,7 +146,7 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
       uint8_t* dst = smem + t % S * C::STAGE;
       const int col = col0 + t * kBC;
       if (tid == 0) {
-        ptx::mbar_arrive_expect_tx(&full[t % S], C::WBYTES + (base ? C::BASE : 0));
+        ptx::mbar_arrive_expect_tx(&full[t % S], C::WBYTES + (base ? quads * 512 * SUBS : 0));
         if constexpr (KN) {  // rank j's row of 64 columns
           tma_load_3d(dst + C::BASE, &map_m, &full[t % S], col, 0, a);
         } else {             // column n's row of ranks
@@ -162,39 +156,19 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
         }
       }
       __syncwarp();
-      if (base && sub < SUBS)
-        ptx::tma_gather4(dst + sub * (kRows * 128) + quad * 512, &map_base, &full[t % S], col + sub * (128 / sizeof(OT)),
-                         row[0], row[1], row[2], row[3]);
+      if (base && sub < SUBS && quad < quads)
+        gather4_once(dst + sub * (kRows * 128) + quad * 512, &map_base, &full[t % S], col + sub * (128 / sizeof(OT)), row,
+                     policy);
     }
     if (!ok) {   // what is in flight lands before the block ends
       int never = 0;
       for (int u = t > S ? t - S : 0; u < t; ++u) ptx::mbar_wait_warp(&full[u % S], (u / S) & 1, &never, kWaitLimitNs);
+      ptx::mbar_wait_warp(&h_full, 0, &never, kWaitLimitNs);
     }
   } else if (warp < kMmaWarp) {
-    // ---- h's terms in, then block by block: accumulator + base, out
+    // ---- block by block: accumulator + base, out
     const int ew = warp - kLoaders / 32, quarter = ew & 3, half = ew >> 2;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const float sc = p.scale ? __ldg(p.scale + a) : 1.f;
-#pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      const int i = et + k * kDrainers, m = i / (RP / 8), j = i % (RP / 8) * 8;
-      uint32_t w[3][4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if constexpr (C::TERMS == 3)
-          split3(v[k][2 * u] * sc, v[k][2 * u + 1] * sc, w[0][u], w[1][u], w[2][u]);
-        else
-          split2(v[k][2 * u] * sc, v[k][2 * u + 1] * sc, w[0][u], w[1][u]);
-      }
-#pragma unroll
-      for (int q = 0; q < C::TERMS; ++q) {
-        const int kk = q * RP + j;
-        *reinterpret_cast<uint4*>(s_h + kk / 64 * (kRows * 128) + swz(m, kk % 64 / 8)) =
-            make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
-      }
-    }
-    ptx::fence_proxy_async_smem();
-    ptx::mbar_arrive(&h_full);
     for (int t = 0; t < blocks; ++t) {
       const bool ok = ptx::mbar_wait_warp(&full[t % S], (t / S) & 1, abort_flag, kWaitLimitNs) &&
                       ptx::mbar_wait_warp(&acc_full[t & 1], (t >> 1) & 1, abort_flag, kWaitLimitNs);
@@ -262,8 +236,7 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
       for (int q = C::TERMS - 1; q >= 0; --q)  // the small terms first
 #pragma unroll
         for (int k = 0; k < RP / 16; ++k) {
-          const int kk = q * (RP / 16) + k;
-          const uint64_t hd = ptx::sw128_kmajor_desc(h + kk / 4 * (kRows * 128)) + kk % 4 * 2;
+          const uint64_t hd = RankTile<RP>::kdesc(h + q * RankTile<RP>::BYTES, k);
           const uint64_t wd = KN ? mn_desc(w + k * 2048, RP * 128)
                                  : ptx::sw128_kmajor_desc(w + k / 4 * (kBC * 128)) + k % 4 * 2;
           ptx::umma_f16(d, hd, wd, ID, q < C::TERMS - 1 || k > 0);
@@ -327,8 +300,9 @@ int launch_expand_rank(const ExpandArgs& p, cudaStream_t s) {
 }  // namespace
 
 int launch_lora_expand(ExpandArgs p, bool kn, int out_dtype, cudaStream_t s) {
-  // columns of a CTA: the narrowest slice (of 128 to 1024) with which two CTAs to an SM are all of them
-  const long long tiles = static_cast<long long>(p.rows) / kRows + p.n;
+  // columns of a CTA: the narrowest slice (of 128 to 1024) with which two CTAs to an SM are all of them;
+  // an adapter's last tile is half full on average
+  const long long tiles = (static_cast<long long>(p.rows) + 64ll * p.n) / kRows + 1;
   p.cols = 1024;
   while (p.cols > 128 && tiles * ((p.N + p.cols / 2 - 1) / (p.cols / 2)) <= 2ll * num_sms()) p.cols /= 2;
   if (out_dtype == MOE_F32) return kn ? launch_expand_rank<true, float>(p, s) : launch_expand_rank<false, float>(p, s);

@@ -20,19 +20,20 @@
 // other's loads.
 //
 // V enters as three bf16 terms (all 24 bits of an fp32 value): G is an fp32
-// sum, and fewer terms would leave their rounding as the largest error in it.
-// Up to rank 32 the terms lie side by side in the MMA's N, which costs nothing
-// (an MMA of N <= 64 is bound by reading its A operand); above, one after the
-// other into the same accumulator.
-//
-// Both V and B are read as they lie in memory, a row's ranks side by side: the
-// MMA takes them with the ranks along N and the rows along K (MN-major), so
-// nothing is transposed on the way.
+// sum, and fewer terms would leave their rounding as the largest error in it
+// (2.7e-6 of the gradient with two, 3.6e-7 of a sum in fp32).  They come split
+// and laid out (lora_tc.cuh): split by every slice's CTA again they took 2700
+// cycles of each 128 rows, more than the MMAs.  Side by side in the MMA's N
+// they take one MMA up to rank 64 (one of 192 columns takes 97 cycles, three of
+// 64 take 153), above one after the other into the same accumulator.  Both V
+// and B lie with a row's ranks side by side, as in memory: the MMA takes them
+// with the ranks along N and the rows along K (MN-major), so nothing is
+// transposed on the way.
 //
 // The first warps load X (tile::gather4, four rows of the plan's order at a
 // time, zeros for a row that is not there; the next 128 rows' ids are fetched a
-// step ahead), eight more prepare V, whose loads run a step ahead too, and
-// empty TMEM, one thread of the last warp issues the MMAs.  gather4 takes a
+// step ahead), eight more empty TMEM, one thread of the last warp issues the
+// MMAs.  gather4 takes a
 // warp about 85 cycles, so eight warps an SM issue them: four where two CTAs
 // share it.  Measured on 117 MB in 224 CTAs: 1.7 TB/s from one warp an SM, 4.4
 // from four, 5.2 from eight, 5.7 from two CTAs of four; cp.async of 16 bytes by
@@ -58,9 +59,9 @@ constexpr int kTerms = 3;
 
 template <int RP, bool PROJ, bool GRAD>
 struct StreamCfg {
-  static constexpr bool STACK = RP <= 32;
+  static constexpr bool STACK = RP <= 64;
   static constexpr int GCOLS = GRAD ? (STACK ? kTerms * RP : RP) : 0;       // TMEM columns of 128 of X's
-  static constexpr int BLOCKS = !GRAD ? 1 : RP <= 16 ? 4 : RP <= 32 ? 2 : RP <= 64 ? 4 : 2;  // 128-column blocks, at most
+  static constexpr int BLOCKS = !GRAD ? 1 : RP <= 16 ? 4 : 2;  // 128-column blocks, at most
   static constexpr int PBUF = GRAD ? 2 : 1;                                 // projection accumulators
   static constexpr int PS = RP + 4;                                         // row stride of P in shared memory: spreads the banks
   static constexpr int PCOL = GRAD ? BLOCKS * GCOLS : 0;                    // their first TMEM column
@@ -69,17 +70,18 @@ struct StreamCfg {
   static constexpr int MSUB = RP * 128;                                     // bytes of A's rows for 64 columns
   static constexpr int RANKS = RankTile<RP>::BYTES;                         // 128 rows of RP ranks: V's term, B's block
   static constexpr int M_ALL = PROJ && GRAD ? BLOCKS * RANKS : 0;           // resident
-  static constexpr int V_ALL = GRAD ? kTerms * RANKS : 0;
   static constexpr int STAGE = 2 * kSub + (PROJ && !GRAD ? 2 * MSUB : 0);
   static constexpr int PER_SM = RP <= 32 || (!GRAD && RP <= 64) ? 2 : 1;
-  static constexpr int LW = PER_SM == 2 ? 4 : 8;                            // warps that load
+  static constexpr int LW = PER_SM == 2 && GRAD ? 4 : 8;                    // warps that load
   static constexpr int MMA_WARP = LW + kDrainers / 32;
   static constexpr int THREADS = (MMA_WARP + 1) * 32;
   static constexpr int GS = RP / 2 + 4;                                     // row stride of a warp's share of G on its way out
   static constexpr int BUDGET = PER_SM == 2 ? 110 * 1024 : 226 * 1024;
-  static constexpr int STAGES_RAW = (BUDGET - M_ALL - V_ALL) / STAGE;
+  static constexpr int V_ONE = GRAD ? RankTile<RP>::IMAGE : 0;
+  static constexpr int VBUF = !GRAD ? 0 : (BUDGET - M_ALL - 2 * V_ONE) / STAGE >= 2 ? 2 : 1;  // two where two stages fit beside
+  static constexpr int STAGES_RAW = (BUDGET - M_ALL - VBUF * V_ONE) / STAGE;
   static constexpr int STAGES = STAGES_RAW > 4 ? 4 : STAGES_RAW;
-  static constexpr int SMEM = STAGES * STAGE + M_ALL + V_ALL + 1024;        // + alignment slack
+  static constexpr int SMEM = STAGES * STAGE + M_ALL + VBUF * V_ONE + 1024;  // + alignment slack
   static_assert(USED <= 512 && STAGES >= 2 && (GRAD || kTile * PS * 4 <= STAGES * STAGE) &&
                     (kDrainers * GS * 4 <= STAGES * STAGE + M_ALL), "TMEM and shared memory");
 };
@@ -119,7 +121,7 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_m = smem + S * C::STAGE;
   uint8_t* s_v = s_m + C::M_ALL;
-  __shared__ __align__(8) uint64_t full[S], empty[S], v_full, step_done[2], p_free[2], drained;
+  __shared__ __align__(8) uint64_t full[S], empty[S], step_done[2], p_free[2], drained;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   volatile int* abort_flag = &s_abort;
@@ -130,7 +132,6 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
       ptx::mbar_init(&full[i], 1);
       ptx::mbar_init(&empty[i], 1);
     }
-    ptx::mbar_init(&v_full, kDrainers);
     ptx::mbar_init(&step_done[0], 1);
     ptx::mbar_init(&step_done[1], 1);
     ptx::mbar_init(&drained, 1);
@@ -145,13 +146,30 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
   const uint32_t CS = GRAD ? 1 : cluster_size();
   const int slot = GRAD ? blockIdx.x : blockIdx.x / CS, slice = GRAD ? blockIdx.y : cluster_rank();
   int a, start, end;
-  if (!find_tile(p.offsets, p.n, p.rows, p.chunk, slot, a, start, end) || a == p.n) return;  // the whole cluster leaves
+  const bool found = find_tile(p.offsets, p.n, p.rows, p.chunk, slot, a, start, end);
   const int W = p.W, R = p.R;
   const int col0 = slice * p.cols;
+  const size_t size = static_cast<size_t>(W) * R;   // G's values of one adapter
+  if (!found || a == p.n) {   // the whole cluster leaves
+    if constexpr (GRAD) {     // the slot of an adapter without rows: its gradient is 0
+      if (a < p.n && p.grad && held_offset(p.offsets, p.n, p.rows, a) >= held_offset(p.offsets, p.n, p.rows, a + 1)) {
+        const size_t first = a * size;
+        const int c1 = min(W, col0 + p.cols), lines = PROJ ? 1 : R;       // [W][R]: one run; [R][W]: one to a rank
+        const int each = PROJ ? (c1 - col0) * R : c1 - col0, bytes = p.grad_f32 ? 4 : 2;
+        for (int i = tid; i < lines * (each / 8); i += C::THREADS) {
+          const size_t o = first + (PROJ ? static_cast<size_t>(col0) * R : static_cast<size_t>(i / (each / 8)) * W + col0) +
+                           i % (each / 8) * 8;
+          for (int u = 0; u < 8 * bytes; u += 16)
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.grad) + o * bytes + u) = make_uint4(0, 0, 0, 0);
+        }
+      }
+    }
+    return;
+  }
   const int blocks = max(0, min(p.cols, W - col0) + kTile - 1) / kTile;  // none behind the last column
   const int steps = (end - start + kTile - 1) / kTile;
   const int tiles = steps * blocks;
-  const bool want_p = PROJ && p.proj, want_g = GRAD && p.grad;
+  const bool want_p = PROJ && (!GRAD || p.proj), want_g = GRAD && p.grad;
 
   if (warp == kMmaWarp) {
     ptx::tmem_alloc(&s_tmem, C::TMEM);
@@ -171,7 +189,10 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
     // 64 (l / Q) .. + 63 of the tile's 128; a row that is not there is taken from behind X, as zeros.
     constexpr int Q = 32 / C::LW;
     const int quad = warp * Q + lane % Q, sub = lane / Q;
-    const bool mine = sub < 2;
+    // the projection alone needs no rows behind the last: what P holds there is not read
+    const int quads = GRAD ? 32 : (end - start + 3) / 4;
+    const bool mine = sub < 2 && quad < quads;
+    const uint64_t policy = ptx::policy_evict_first();
     int next[4], row[4];
     auto fetch_ids = [&](int step) {
 #pragma unroll
@@ -181,6 +202,9 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
       }
     };
     fetch_ids(0);
+    // the first tile slot of this chunk's rows
+    const int first = held_offset(p.offsets, p.n, p.rows, a);
+    const uint8_t* image = p.V + static_cast<size_t>(first / kTile + a + (start - first) / kTile) * RT::IMAGE;
     bool ok = true;
     int t = 0;
     for (int step = 0; step < steps && ok; ++step) {
@@ -196,7 +220,8 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
         uint8_t* dst = smem + t % S * C::STAGE;
         const int col = col0 + b * kTile;
         if (tid == 0) {
-          ptx::mbar_arrive_expect_tx(&full[t % S], C::STAGE + (PROJ && GRAD && step == 0 ? C::RANKS : 0));
+          ptx::mbar_arrive_expect_tx(&full[t % S], C::STAGE - (32 - quads) * 1024 + (PROJ && GRAD && step == 0 ? C::RANKS : 0) +
+                                                         (want_g && b == 0 ? C::V_ONE : 0));
           if constexpr (PROJ && !GRAD) {   // A's columns of this tile
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -212,8 +237,20 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
         }
         __syncwarp();
         if (mine)
-          ptx::tma_gather4(dst + sub * kSub + quad * 512, &map_x, &full[t % S], col + sub * 64, row[0], row[1], row[2],
-                           row[3]);
+          gather4_once(dst + sub * kSub + quad * 512, &map_x, &full[t % S], col + sub * 64, row, policy);
+        if constexpr (GRAD) {
+          if (want_g && b == 0 && warp == 0) {   // V's terms of these rows, where a step's MMAs have left theirs
+            constexpr int VB = C::VBUF;
+            if (step >= VB && !ptx::mbar_wait_warp(&step_done[(step - VB) & 1], ((step - VB) >> 1) & 1, abort_flag, kWaitLimitNs)) {
+              give_up();
+              ok = false;
+              ++t;
+              break;
+            }
+            if (lane == 0)
+              bulk_load(s_v + step % VB * C::V_ONE, image + static_cast<size_t>(step) * RT::IMAGE, C::V_ONE, &full[t % S]);
+          }
+        }
       }
     }
     if (!ok) {   // what is in flight lands before the block ends
@@ -221,107 +258,49 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
       for (int u = t > S ? t - S : 0; u < t; ++u) ptx::mbar_wait_warp(&full[u % S], (u / S) & 1, &never, kWaitLimitNs);
     }
   } else if (warp < kMmaWarp) {
-    // ---- V in, P out, and at the end G.  Two warps to a quarter of TMEM's lanes, half the columns each.
+    // ---- P out, and at the end G.  Two warps to a quarter of TMEM's lanes, half the columns each.
     const int et = tid - kLoaders, ew = warp - kLoaders / 32, quarter = ew & 3, half = ew >> 2;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const float sc = PROJ && GRAD && p.scale ? __ldg(p.scale + a) : 1.f;
-    constexpr int NP = RP * 16 / kDrainers;   // a thread's pieces of 8 ranks
     constexpr int HC = RP / 2 > 32 ? 32 : RP / 2;   // TMEM columns read at once
-    int id[NP];
-    float v[NP][8];
-    auto fetch_ids = [&](int step) {  // the rows of V of its pieces
-#pragma unroll
-      for (int k = 0; k < NP; ++k) {
-        const int at = start + step * kTile + (et + k * kDrainers) / (RP / 8);
-        id[k] = at < end ? (PROJ ? __ldg(p.order + at) : at) : -1;
-        if (PROJ && id[k] >= p.rows) id[k] = -1;
-      }
-    };
-    auto fetch_v = [&]() {
-#pragma unroll
-      for (int k = 0; k < NP; ++k) {
-        const int j = (et + k * kDrainers) % (RP / 8) * 8;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-        if (id[k] >= 0 && j < R) {
-          const float4* from = reinterpret_cast<const float4*>(p.V + static_cast<size_t>(id[k]) * R + j);
-          x = __ldg(from), y = __ldg(from + 1);
-        }
-        v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
-        v[k][4] = y.x, v[k][5] = y.y, v[k][6] = y.z, v[k][7] = y.w;
-      }
-    };
-    auto store_v = [&]() {  // as three terms
-#pragma unroll
-      for (int k = 0; k < NP; ++k) {
-        const int i = et + k * kDrainers;
-        const uint32_t at = RT::at(i / (RP / 8), i % (RP / 8));
-        uint32_t w[kTerms][4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) split3(v[k][2 * u] * sc, v[k][2 * u + 1] * sc, w[0][u], w[1][u], w[2][u]);
-#pragma unroll
-        for (int q = 0; q < kTerms; ++q)
-          *reinterpret_cast<uint4*>(s_v + q * C::RANKS + at) = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
-      }
-      ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(&v_full);
-    };
-    if constexpr (GRAD) {
-      if (want_g) {   // past the last step the ids are -1 and nothing is read
-        fetch_ids(0);
-        fetch_v();
-        fetch_ids(1);
-        store_v();
-        fetch_v();
-        fetch_ids(2);
-      }
-    }
     bool ok = true;
-    for (int step = 0; step < (GRAD ? steps : 0); ++step) {
-      // the step's MMAs are done: V may be replaced, P is complete
+    for (int step = 0; step < (GRAD && want_p ? steps : 0); ++step) {
+      // the step's MMAs are done: P is complete
       if (!ptx::mbar_wait_warp(&step_done[step & 1], (step >> 1) & 1, abort_flag, kWaitLimitNs)) {
         give_up();
         ok = false;
         break;
       }
-      if constexpr (GRAD) {
-        if (want_g && step + 1 < steps) {
-          store_v();
-          fetch_v();
-          fetch_ids(step + 3);
-        }
-      }
       if constexpr (PROJ) {
-        if (want_p) {
-          ptx::tc_fence_after();
-          const int at = start + step * kTile + quarter * 32 + lane;
-          float* o = p.proj + (static_cast<size_t>(slice) * p.rows + at) * R;
-          const uint32_t from = tmem + lane_base + C::PCOL + step % C::PBUF * RP;
+        ptx::tc_fence_after();
+        const int at = start + step * kTile + quarter * 32 + lane;
+        float* o = p.proj + (static_cast<size_t>(slice) * p.rows + at) * R;
+        const uint32_t from = tmem + lane_base + C::PCOL + step % C::PBUF * RP;
 #pragma unroll
-          for (int u = 0; u < RP / 2; u += HC) {
-            uint32_t r[HC];
-            __syncwarp();
-            tmem_ld(from + half * (RP / 2) + u, r);
-            ptx::tmem_ld_wait();
+        for (int u = 0; u < RP / 2; u += HC) {
+          uint32_t r[HC];
+          __syncwarp();
+          tmem_ld(from + half * (RP / 2) + u, r);
+          ptx::tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < HC; e += 8) {
-              const int j = half * (RP / 2) + u + e;
-              if (at >= end || j >= R) continue;
-              float x[8];
+          for (int e = 0; e < HC; e += 8) {
+            const int j = half * (RP / 2) + u + e;
+            if (at >= end || j >= R) continue;
+            float x[8];
 #pragma unroll
-              for (int q = 0; q < 8; ++q) x[q] = __uint_as_float(r[e + q]) * sc;
-              store32(o + j, x);
-            }
+            for (int q = 0; q < 8; ++q) x[q] = __uint_as_float(r[e + q]) * sc;
+            store32(o + j, x);
           }
-          ptx::tc_fence_before();
-          ptx::mbar_arrive(&p_free[step % C::PBUF]);
         }
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(&p_free[step % C::PBUF]);
       }
     }
     if constexpr (!GRAD) {   // the slice's P to shared memory, over the stages: their MMAs are done
       float* s_p = reinterpret_cast<float*>(smem) + (quarter * 32 + lane) * C::PS + half * (RP / 2);
       if (blocks == 0) {
         for (int j = 0; j < RP / 2; j += 4) *reinterpret_cast<float4*>(s_p + j) = make_float4(0.f, 0.f, 0.f, 0.f);
-      } else if (ptx::mbar_wait_warp(&step_done[0], 0, abort_flag, kWaitLimitNs)) {
+      } else if (ptx::mbar_wait_warp(&drained, 0, abort_flag, kWaitLimitNs)) {
         ptx::tc_fence_after();
 #pragma unroll
         for (int j = 0; j < RP / 2; j += 8) {
@@ -338,12 +317,15 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
       }
     }
     if constexpr (GRAD) {
+      if (want_g && ok && !ptx::mbar_wait_warp(&drained, 0, abort_flag, kWaitLimitNs)) {
+        give_up();
+        ok = false;
+      }
       if (want_g && ok) {
         ptx::tc_fence_after();
         const int first = held_offset(p.offsets, p.n, p.rows, a), last = held_offset(p.offsets, p.n, p.rows, a + 1);
         const bool whole = last - first <= p.chunk;  // no other chunk adds to it
-        const size_t size = static_cast<size_t>(W) * R;
-        float* part = p.part + static_cast<size_t>(slot) * size;
+        float* part = p.part + (part_slot(first, p.chunk) + (start - first) / p.chunk) * size;
         float* g32 = static_cast<float*>(p.grad) + a * size;
         __nv_bfloat16* g16 = static_cast<__nv_bfloat16*>(p.grad) + a * size;
         // [W][R]: through shared memory (over the stages and B: the MMAs are done), where a thread holds a
@@ -397,9 +379,8 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
     bool ok = true;
     int t = 0;
     for (int step = 0; step < steps && blocks > 0 && ok; ++step) {
-      if (want_g) ok = ptx::mbar_wait(&v_full, step & 1, abort_flag, kWaitLimitNs);
       if (want_p && step >= C::PBUF)
-        ok = ok && ptx::mbar_wait(&p_free[step % C::PBUF], (step / C::PBUF - 1) & 1, abort_flag, kWaitLimitNs);
+        ok = ptx::mbar_wait(&p_free[step % C::PBUF], (step / C::PBUF - 1) & 1, abort_flag, kWaitLimitNs);
       for (int b = 0; b < blocks && ok; ++b, ++t) {
         ok = ptx::mbar_wait(&full[t % S], (t / S) & 1, abort_flag, kWaitLimitNs);
         if (!ok) break;
@@ -416,7 +397,7 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
           }
         }
         if (want_g) {
-          const uint32_t v = ptx::smem_u32(s_v);
+          const uint32_t v = ptx::smem_u32(s_v) + (C::VBUF == 2 ? (step & 1) * C::V_ONE : 0);
           const uint32_t d = tmem + b * C::GCOLS;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {  // 16 rows at a time
@@ -435,10 +416,10 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
       }
       if (ok) ptx::umma_commit(&step_done[step & 1]);
     }
+    ptx::umma_commit(&drained);
     if (!ok) {
       give_up();
       int never = 0;   // what was issued is waited for before TMEM goes
-      ptx::umma_commit(&drained);
       ptx::mbar_wait(&drained, 0, &never, kWaitLimitNs);
     }
   }
@@ -453,18 +434,28 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
     __syncwarp();
     cluster_arrive();
     cluster_wait();
+    const float sc = p.scale ? __ldg(p.scale + a) : 1.f;
+    uint8_t* image = p.image + static_cast<size_t>(slot) * RT::IMAGE;
     for (int i = tid; i < kTile / static_cast<int>(CS) * (RP / 4); i += C::THREADS) {
       const int m = i / (RP / 4) * static_cast<int>(CS) + slice, j = i % (RP / 4) * 4;
-      if (start + m >= end || j >= R) continue;
+      if (start + m >= end) continue;   // what the image holds there reaches that row of the product alone
       const float4* from = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem) + m * C::PS + j);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (uint32_t q = 0; q < CS; ++q) {
-        const float4 u = ld_cluster(from, q);
-        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
-      }
-      *reinterpret_cast<float4*>(p.proj + static_cast<size_t>(start + m) * R + j) = v;
-      const int r = p.h_out ? __ldg(p.order + start + m) : -1;
+      float4 x[8], v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (uint32_t q = 0; q < 8; ++q)   // all in flight
+        if (q < CS) x[q] = ld_cluster(from, q);
+#pragma unroll
+      for (uint32_t q = 0; q < 8; ++q)
+        if (q < CS) v.x += x[q].x, v.y += x[q].y, v.z += x[q].z, v.w += x[q].w;
+      if (j >= R) v = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int r = p.h_out && j < R ? __ldg(p.order + start + m) : -1;
       if (r >= 0 && r < p.rows) *reinterpret_cast<float4*>(p.h_out + static_cast<size_t>(r) * R + j) = v;
+      uint32_t w[kTerms][2];
+      split3(v.x * sc, v.y * sc, w[0][0], w[1][0], w[2][0]);
+      split3(v.z * sc, v.w * sc, w[0][1], w[1][1], w[2][1]);
+#pragma unroll
+      for (int q = 0; q < kTerms; ++q)
+        *reinterpret_cast<uint2*>(image + q * RT::BYTES + RT::at(m, j / 8) + j % 8 * 2) = make_uint2(w[q][0], w[q][1]);
     }
     __syncwarp();
     cluster_arrive();   // no CTA leaves while another one reads its shared memory
@@ -524,11 +515,12 @@ bool make_adapter_map(CUtensorMap* m, const void* base, uint64_t n, uint64_t row
   return true;
 }
 
-int lora_stream_max_cols(int R) {
-  return kTile * (R <= 16   ? StreamCfg<16, true, true>::BLOCKS
-                  : R <= 32 ? StreamCfg<32, true, true>::BLOCKS
-                  : R <= 64 ? StreamCfg<64, true, true>::BLOCKS
-                            : StreamCfg<128, true, true>::BLOCKS);
+int lora_stream_max_cols(int R, bool proj) {
+  auto blocks = [=](auto with, auto without) { return kTile * (proj ? decltype(with)::BLOCKS : decltype(without)::BLOCKS); };
+  return R <= 16   ? blocks(StreamCfg<16, true, true>(), StreamCfg<16, false, true>())
+         : R <= 32 ? blocks(StreamCfg<32, true, true>(), StreamCfg<32, false, true>())
+         : R <= 64 ? blocks(StreamCfg<64, true, true>(), StreamCfg<64, false, true>())
+                   : blocks(StreamCfg<128, true, true>(), StreamCfg<128, false, true>());
 }
 
 int launch_lora_stream(const StreamArgs& p, StreamKind kind, cudaStream_t s) {
