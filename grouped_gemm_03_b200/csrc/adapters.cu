@@ -3,23 +3,26 @@
 //   out[r] = base[r] + s_a (x[r] A_a^T) B_a^T,   a = the row's adapter.
 // A_a is [R, d], B_a [N, R] (both K-major like the library's weights).
 //
-// Forward, one launch.  A tile is up to MT rows of one adapter (16, or 64 when
-// adapters have more rows); a cluster of up to eight CTAs shares it.  CTA q
-// multiplies the q-th slice of x's columns with A_a, the cluster's partial
-// x A^T meet through distributed shared memory in rank order, and CTA q then
-// adds its slice of the N output columns.  x, base and out cross HBM once and
-// h = x A^T never leaves the chip (unless the caller wants it kept).
+// Forward.  Up to 16 rows to an adapter (decode: a token or so to a request) one
+// launch does it: a tile is up to 16 rows of one adapter, a cluster of up to
+// eight CTAs shares it.  CTA q multiplies the q-th slice of x's columns with
+// A_a, the cluster's partial x A^T meet through distributed shared memory in
+// rank order, and CTA q then adds its slice of the N output columns.  x, base
+// and out cross HBM once and h = x A^T never leaves the chip (unless the caller
+// wants it kept).  It is bound by memory and latency, so operands go from global
+// memory straight into mma fragments, 16 bytes a lane: a product does not depend
+// on the order of its inner index, so lane c of a quad takes 8 consecutive inner
+// elements as its share of two k16 steps, and the columns of an output block are
+// dealt to the mma's n index so that a lane holds 8 consecutive ones.  No
+// shared-memory staging, full sectors both ways.
 //
-// The kernel is bound by memory (2 R FLOP per element read at R <= 128), so
-// operands go from global memory straight into mma fragments, 16 bytes a lane:
-// a product does not depend on the order of its inner index, so lane c of a
-// quad takes 8 consecutive inner elements as its share of two k16 steps, and
-// the columns of an output block are dealt to the mma's n index so that a lane
-// holds 8 consecutive ones.  No shared-memory staging, full sectors both ways.
+// With more rows the two products are launches of their own on tiles of 128
+// rows (lora_stream.cu, lora_expand.cu).
 //
 // h enters the second product as two bf16 terms (hi + lo, 16 bits of mantissa
-// together): one bf16 term alone would put its own rounding, 2^-9 a value,
-// beside that of a bf16 result and dominate an fp32 one.
+// together) for a bf16 result and as three (all 24) for an fp32 one: one bf16
+// term alone would put its own rounding, 2^-9 a value, beside that of a bf16
+// result, and two left 1e-6 of an fp32 one.
 #include <cstdint>
 
 #include "common.cuh"
@@ -154,28 +157,28 @@ struct LoraArgs {
   int kslice, nslice;   // columns of x / of out a CTA of the cluster takes, multiples of 32
 };
 
-template <int RP, int MT>
+constexpr int MT = 16;   // rows of a tile
+constexpr int WK = 8;    // warps along the columns
+
+template <int RP, int TERMS>
 struct LoraTile {
-  static constexpr int MW = RP <= 64 && MT >= 32 ? 2 : 1;   // m16 tiles a warp holds
-  static constexpr int WM = MT / (16 * MW);                 // warps along the rows
-  static constexpr int WK = 8 / WM;                         // warps along the columns
-  static constexpr int HS = RP + 8;                         // row stride of the bf16 h terms: spreads the banks
-  static constexpr int RED = WK * MT * RP * 4;              // the warps' partial sums; then h's two terms
-  static constexpr int HB = 2 * MT * HS * 2;
+  static constexpr int HS = RP + 8;                         // row stride of h's bf16 terms: spreads the banks
+  static constexpr int RED = WK * MT * RP * 4;              // the warps' partial sums; then h's terms
+  static constexpr int HB = TERMS * MT * HS * 2;
   static constexpr int SMEM = (RED > HB ? RED : HB) + MT * RP * 4;
   static constexpr int UK = RP <= 16 ? 4 : RP <= 64 ? 2 : 1;  // k32 steps loaded ahead
 };
 
-template <int RP, int MT, typename OT>
+template <int RP, typename OT>
 __global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraArgs p) {
-  using L = LoraTile<RP, MT>;
-  constexpr int MW = L::MW, WM = L::WM, WK = L::WK, HS = L::HS;
+  constexpr int TERMS = sizeof(OT) == 4 ? 3 : 2;
+  using L = LoraTile<RP, TERMS>;
+  constexpr int HS = L::HS;
   pdl_wait();
   pdl_launch_dependents();
   extern __shared__ __align__(16) uint8_t s_raw[];
   float* s_red = reinterpret_cast<float*>(s_raw);                        // [WK][MT][RP]
-  __nv_bfloat16* s_hi = reinterpret_cast<__nv_bfloat16*>(s_raw);         // [MT][HS], after the sums are read
-  __nv_bfloat16* s_lo = s_hi + MT * HS;
+  __nv_bfloat16* s_h = reinterpret_cast<__nv_bfloat16*>(s_raw);          // [TERMS][MT][HS], after the sums are read
   float* s_part = reinterpret_cast<float*>(s_raw + L::SMEM - MT * RP * 4);  // [MT][RP]: this CTA's slice of h
   __shared__ int s_row[MT];
 
@@ -211,37 +214,30 @@ __global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraArgs p) {
   }
 
   // ---- h over this CTA's columns of x
-  const int wm = warp % WM, wk = warp / WM;
   {
-    float acc[MW][RP / 8][4];
+    float acc[RP / 8][4];
 #pragma unroll
-    for (int m = 0; m < MW; ++m)
+    for (int j = 0; j < RP / 8; ++j)
 #pragma unroll
-      for (int j = 0; j < RP / 8; ++j)
+      for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+    const __nv_bfloat16* xr[2];
+    bool xl[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.f;
-    const __nv_bfloat16* xr[MW][2];
-    bool xl[MW][2];
-#pragma unroll
-    for (int m = 0; m < MW; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = s_row[(wm * MW + m) * 16 + g + 8 * h];
-        xl[m][h] = r >= 0;
-        xr[m][h] = p.x + static_cast<size_t>(r >= 0 ? r : 0) * p.d + c * 8;
-      }
+    for (int h = 0; h < 2; ++h) {
+      const int r = s_row[g + 8 * h];
+      xl[h] = r >= 0;
+      xr[h] = p.x + static_cast<size_t>(r >= 0 ? r : 0) * p.d + c * 8;
+    }
     const __nv_bfloat16* Ar = p.A + (static_cast<size_t>(a) * p.R + g) * p.d + c * 8;
     const int k0 = rank * p.kslice, k1 = min(p.d, k0 + p.kslice);
-    for (int kb = k0 + wk * 32; kb < k1; kb += WK * 32 * L::UK) {
-      uint4 xv[L::UK][MW][2], av[L::UK][RP / 8];
+    for (int kb = k0 + warp * 32; kb < k1; kb += WK * 32 * L::UK) {
+      uint4 xv[L::UK][2], av[L::UK][RP / 8];
 #pragma unroll
       for (int u = 0; u < L::UK; ++u) {
         const int k = kb + u * WK * 32;
         const bool in = k + c * 8 < k1;
 #pragma unroll
-        for (int m = 0; m < MW; ++m)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) xv[u][m][h] = in && xl[m][h] ? ldg_stream(xr[m][h] + k) : make_uint4(0, 0, 0, 0);
+        for (int h = 0; h < 2; ++h) xv[u][h] = in && xl[h] ? ldg_stream(xr[h] + k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int j = 0; j < RP / 8; ++j)
           av[u][j] = in && j * 8 + g < p.R ? ldg16(Ar + static_cast<size_t>(j * 8) * p.d + k) : make_uint4(0, 0, 0, 0);
@@ -249,22 +245,17 @@ __global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraArgs p) {
 #pragma unroll
       for (int u = 0; u < L::UK; ++u)
 #pragma unroll
-        for (int m = 0; m < MW; ++m)
-#pragma unroll
-          for (int j = 0; j < RP / 8; ++j) {
-            mma16816(acc[m][j], xv[u][m][0].x, xv[u][m][1].x, xv[u][m][0].y, xv[u][m][1].y, av[u][j].x, av[u][j].y);
-            mma16816(acc[m][j], xv[u][m][0].z, xv[u][m][1].z, xv[u][m][0].w, xv[u][m][1].w, av[u][j].z, av[u][j].w);
-          }
+        for (int j = 0; j < RP / 8; ++j) {
+          mma16816(acc[j], xv[u][0].x, xv[u][1].x, xv[u][0].y, xv[u][1].y, av[u][j].x, av[u][j].y);
+          mma16816(acc[j], xv[u][0].z, xv[u][1].z, xv[u][0].w, xv[u][1].w, av[u][j].z, av[u][j].w);
+        }
     }
 #pragma unroll
-    for (int m = 0; m < MW; ++m)
+    for (int h = 0; h < 2; ++h) {
+      float* o = s_red + (static_cast<size_t>(warp) * MT + g + 8 * h) * RP + 2 * c;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float* o = s_red + (static_cast<size_t>(wk) * MT + (wm * MW + m) * 16 + g + 8 * h) * RP + 2 * c;
-#pragma unroll
-        for (int j = 0; j < RP / 8; ++j)
-          *reinterpret_cast<float2*>(o + 8 * j) = make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
-      }
+      for (int j = 0; j < RP / 8; ++j) *reinterpret_cast<float2*>(o + 8 * j) = make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
+    }
   }
   __syncthreads();
   for (int i = tid; i < MT * RP / 4; i += kLoraThreads) {
@@ -288,43 +279,40 @@ __global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraArgs p) {
     const int m = i / (RP / 4), j = i % (RP / 4) * 4;
     if (p.h_out && m % CS == rank && s_row[m] >= 0 && j < p.R)
       *reinterpret_cast<float4*>(p.h_out + static_cast<size_t>(s_row[m]) * p.R + j) = v;
-    split_store(s_hi + m * HS + j, s_lo + m * HS + j, v, sc);
+    uint32_t w[3][2];
+    split3(v.x * sc, v.y * sc, w[0][0], w[1][0], w[2][0]);
+    split3(v.z * sc, v.w * sc, w[0][1], w[1][1], w[2][1]);
+#pragma unroll
+    for (int q = 0; q < TERMS; ++q)
+      *reinterpret_cast<uint2*>(s_h + (q * MT + m) * HS + j) = make_uint2(w[q][0], w[q][1]);
   }
   cluster_arrive();  // done with the others' shared memory; waited for before this CTA ends
   __syncthreads();
 
   // ---- out over this CTA's columns
-  uint32_t hh[MW][RP / 16][4], hl[MW][RP / 16][4];
+  uint32_t hf[TERMS][RP / 16][4];
 #pragma unroll
-  for (int m = 0; m < MW; ++m) {
-    const int r = (wm * MW + m) * 16 + g;
-    load_terms<RP>(s_hi + r * HS, s_hi + (r + 8) * HS, c, hh[m]);
-    load_terms<RP>(s_lo + r * HS, s_lo + (r + 8) * HS, c, hl[m]);
+  for (int q = 0; q < TERMS; ++q) load_terms<RP>(s_h + (q * MT + g) * HS, s_h + (q * MT + g + 8) * HS, c, hf[q]);
+  size_t ro[2];
+  bool rl[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = s_row[g + 8 * h];
+    rl[h] = r >= 0;
+    ro[h] = static_cast<size_t>(r >= 0 ? r : 0) * p.N + c * 8;
   }
-  size_t ro[MW][2];
-  bool rl[MW][2];
-#pragma unroll
-  for (int m = 0; m < MW; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = s_row[(wm * MW + m) * 16 + g + 8 * h];
-      rl[m][h] = r >= 0;
-      ro[m][h] = static_cast<size_t>(r >= 0 ? r : 0) * p.N + c * 8;
-    }
   // the mma's n index g of block t is column (g / 2) * 8 + 2 t + g % 2 of 32
   const __nv_bfloat16* Bc = p.B + (static_cast<size_t>(a) * p.N + (g >> 1) * 8 + (g & 1)) * p.R;
-  for (int nb = n0 + wk * 32; nb < n1; nb += WK * 32) {
-    float acc[MW][4][4];
+  for (int nb = n0 + warp * 32; nb < n1; nb += WK * 32) {
+    float acc[4][4];
     const bool in = nb + c * 8 < n1;
 #pragma unroll
-    for (int m = 0; m < MW; ++m)
+    for (int h = 0; h < 2; ++h) {
+      float v[8] = {};
+      if (base && in && rl[h]) load8(base + ro[h] + nb, v);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float v[8] = {};
-        if (base && in && rl[m][h]) load8(base + ro[m][h] + nb, v);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) acc[m][t][2 * h] = v[2 * t], acc[m][t][2 * h + 1] = v[2 * t + 1];
-      }
+      for (int t = 0; t < 4; ++t) acc[t][2 * h] = v[2 * t], acc[t][2 * h + 1] = v[2 * t + 1];
+    }
     const bool bin = nb + (g >> 1) * 8 < n1;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -333,54 +321,45 @@ __global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraArgs p) {
 #pragma unroll
       for (int k = 0; k < RP / 16; ++k)
 #pragma unroll
-        for (int m = 0; m < MW; ++m) {
-          mma16816(acc[m][t], hl[m][k][0], hl[m][k][1], hl[m][k][2], hl[m][k][3], b[k][0], b[k][1]);
-          mma16816(acc[m][t], hh[m][k][0], hh[m][k][1], hh[m][k][2], hh[m][k][3], b[k][0], b[k][1]);
-        }
+        for (int q = TERMS - 1; q >= 0; --q)   // the small terms first
+          mma16816(acc[t], hf[q][k][0], hf[q][k][1], hf[q][k][2], hf[q][k][3], b[k][0], b[k][1]);
     }
 #pragma unroll
-    for (int m = 0; m < MW; ++m)
+    for (int h = 0; h < 2; ++h) {
+      if (!in || !rl[h]) continue;
+      float v[8];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (!in || !rl[m][h]) continue;
-        float v[8];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) v[2 * t] = acc[m][t][2 * h], v[2 * t + 1] = acc[m][t][2 * h + 1];
-        store8(out + ro[m][h] + nb, v);
-      }
+      for (int t = 0; t < 4; ++t) v[2 * t] = acc[t][2 * h], v[2 * t + 1] = acc[t][2 * h + 1];
+      store8(out + ro[h] + nb, v);
+    }
   }
   cluster_wait();
 }
 
-template <int RP, int MT, typename OT>
-int launch_lora_tile(const LoraArgs& p, int cs, cudaStream_t s) {
-  using L = LoraTile<RP, MT>;
-  auto kernel = lora_kernel<RP, MT, OT>;
+template <int RP, typename OT>
+int launch_lora_tiles(LoraArgs& p, cudaStream_t s) {
+  using L = LoraTile<RP, sizeof(OT) == 4 ? 3 : 2>;
+  auto kernel = lora_kernel<RP, OT>;
   static std::atomic<uint64_t> done{0};
   const int st = allow_smem(done, kernel, L::SMEM);
   if (st != MOE_OK) return st;
-  const long long tiles = tile_slots<MT>(p.rows, p.n);
-  return launch_cluster("lora_kernel", kernel, dim3(static_cast<unsigned>(tiles * cs)), dim3(kLoraThreads), L::SMEM, cs, s, p);
-}
-
-template <int RP, typename OT>
-int launch_lora_rows(LoraArgs& p, cudaStream_t s) {
   // CTAs to fill the SMs twice, each with at least 128 columns of the wider side
-  const long long tiles = static_cast<long long>(p.rows) / 16 + p.n;
+  const long long tiles = static_cast<long long>(p.rows) / MT + p.n;
   const int widest = p.d > p.N ? p.d : p.N;
   int cs = 1;
   while (cs < 8 && tiles * cs < 4ll * num_sms() && widest >= cs * 2 * 128) cs *= 2;
   p.kslice = ((p.d + cs - 1) / cs + 31) / 32 * 32;
   p.nslice = ((p.N + cs - 1) / cs + 31) / 32 * 32;
-  return launch_lora_tile<RP, 16, OT>(p, cs, s);
+  return launch_cluster("lora_kernel", kernel, dim3(static_cast<unsigned>(tile_slots<MT>(p.rows, p.n) * cs)),
+                        dim3(kLoraThreads), L::SMEM, cs, s, p);
 }
 
 template <typename OT>
 int launch_lora_rank(LoraArgs& p, cudaStream_t s) {
-  if (p.R <= 16) return launch_lora_rows<16, OT>(p, s);
-  if (p.R <= 32) return launch_lora_rows<32, OT>(p, s);
-  if (p.R <= 64) return launch_lora_rows<64, OT>(p, s);
-  return launch_lora_rows<128, OT>(p, s);
+  if (p.R <= 16) return launch_lora_tiles<16, OT>(p, s);
+  if (p.R <= 32) return launch_lora_tiles<32, OT>(p, s);
+  if (p.R <= 64) return launch_lora_tiles<64, OT>(p, s);
+  return launch_lora_tiles<128, OT>(p, s);
 }
 
 }  // namespace

@@ -28,8 +28,7 @@ constexpr int kBalThreads = 256;
 constexpr int kBalMinChunk = 32;     // tokens of one block, at least
 constexpr int kBalMaxChunks = 592;   // blocks of the first pass: four on each of 148 SMs
 constexpr int kBalSmall = 512;       // tokens up to which one cluster does both passes
-constexpr int kFinThreads = 1024;
-constexpr int kFinCluster = 8;       // CTAs of the second pass, each a slice of the experts
+constexpr int kFinCluster = 8;       // CTAs of a small batch's second pass, each a slice of the experts
 
 // A row of E values over L lanes, V values a lane in pieces of C (16 bytes):
 // lane l holds columns (q * L + l) * C + c as value q * C + c.
@@ -182,6 +181,9 @@ struct BalanceArgs {
   int32_t* part_c;      // [chunks + S][E]
   int32_t* part_n;      // [chunks + S]
   int32_t* part_err;    // [chunks]
+  float* share;         // of the loss, [S][groups of kFinCols experts]
+  int32_t* tokens;      // [S]
+  int* done;            // blocks of the second pass that have finished
   float* loss;
   int32_t* counts;
   float* prob;
@@ -199,6 +201,7 @@ __device__ void balance_partial(const BalanceArgs& a, float* s_mem) {
   int* s_c = reinterpret_cast<int*>(s_mem + (kBalThreads / 32) * width);  // [E]
   __shared__ int s_err;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (blockIdx.x == 0 && tid == 0) *a.done = 0;
   const int l = lane % L, group = tid / L, groups = kBalThreads / L;
   const T* logits = static_cast<const T*>(a.logits);
   const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
@@ -289,11 +292,11 @@ __device__ void balance_partial(const BalanceArgs& a, float* s_mem) {
   if (tid == 0) a.part_err[blockIdx.x] = s_err;
 }
 
-// Second pass, one cluster: CTA r reduces its slice of the experts over the
-// slots of every sequence, `w` threads to a column and `g` sequences at once;
-// the CTAs' shares of the loss meet in rank order.
-template <int NT>
+// Second pass of a small batch, within the cluster: CTA r reduces its slice of
+// the experts over the slots of every sequence, `w` threads to a column and `g`
+// sequences at once; the CTAs' shares of the loss meet in rank order.
 __device__ void balance_finish(const BalanceArgs& a, int cols, int w) {
+  constexpr int NT = kBalThreads;
   __shared__ float s_warp[NT / 32];
   __shared__ float s_loss[kFinCluster];
   const int tid = threadIdx.x;
@@ -384,13 +387,102 @@ __global__ void __launch_bounds__(kBalThreads) balance_partial_kernel(const Bala
   balance_partial<T, V>(a, s_mem);
 }
 
-__global__ void __launch_bounds__(kFinThreads) __cluster_dims__(kFinCluster, 1, 1)
-    balance_finish_kernel(const BalanceArgs a, int cols, int w) {
+// Second pass of a large one: a task is a sequence's 8 columns, a block's (BLOCK)
+// or a warp's; lane l adds column l % 8 over every fourth slot of its warp's.
+// The block that finishes last counts the sequences that have tokens and adds
+// the tasks' shares of the loss, in a fixed order whichever block it is.
+constexpr int kFinCols = 8;
+
+template <bool BLOCK>
+__global__ void __launch_bounds__(kBalThreads) balance_finish_kernel(const BalanceArgs a) {
   pdl_wait();
   pdl_launch_dependents();
-  // every CTA of the cluster runs before another one writes to its shared memory
-  cluster_barrier();
-  balance_finish<kFinThreads>(a, cols, w);
+  constexpr int WARPS = kBalThreads / 32;
+  __shared__ float s_q[WARPS][kFinCols];
+  __shared__ int s_c[WARPS][kFinCols], s_n[WARPS];
+  __shared__ float s_sum[WARPS];
+  __shared__ bool s_last;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.E;
+  const int slabs = (E + kFinCols - 1) / kFinCols;
+  const long long tasks = static_cast<long long>(a.S) * slabs, step = BLOCK ? gridDim.x : gridDim.x * WARPS;
+  for (long long i = BLOCK ? blockIdx.x : blockIdx.x * WARPS + warp; i < tasks; i += step) {
+    const int s = static_cast<int>(i / slabs), slab = static_cast<int>(i % slabs), e = slab * kFinCols + lane % 8;
+    const int t0 = a.off ? max(0, min(a.T, a.off[s])) : 0, t1 = a.off ? max(0, min(a.T, a.off[s + 1])) : a.T;
+    const int first = t1 > t0 ? t0 / a.chunk + s : 0, last = t1 > t0 ? (t1 - 1) / a.chunk + s + 1 : 0;
+    float q = 0.f;
+    int c = 0, n = 0;
+#pragma unroll 4
+    for (int u = first + lane / 8 + (BLOCK ? warp * 4 : 0); u < last; u += BLOCK ? WARPS * 4 : 4) {
+      if (e < E) {
+        q += a.part_q[static_cast<size_t>(u) * E + e];
+        c += a.part_c[static_cast<size_t>(u) * E + e];
+      }
+      n += a.part_n[u];
+    }
+#pragma unroll
+    for (int o = 8; o < 32; o *= 2) {
+      q += __shfl_xor_sync(0xffffffffu, q, o);
+      c += __shfl_xor_sync(0xffffffffu, c, o);
+      n += __shfl_xor_sync(0xffffffffu, n, o);
+    }
+    if (BLOCK) {
+      if (lane < kFinCols) s_q[warp][lane] = q, s_c[warp][lane] = c;
+      if (lane == 0) s_n[warp] = n;
+      __syncthreads();
+      q = 0.f, c = 0, n = 0;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) q += s_q[w][lane % 8], c += s_c[w][lane % 8], n += s_n[w];
+      __syncthreads();
+      if (warp) continue;
+    }
+    const float nf = static_cast<float>(n);
+    float share = 0.f;
+    if (e < E) {
+      if (lane < kFinCols) {
+        a.counts[static_cast<size_t>(s) * E + e] = c;
+        if (a.prob) a.prob[static_cast<size_t>(s) * E + e] = n > 0 ? __fdiv_rn(q, nf) : 0.f;
+      }
+      share = n > 0 ? static_cast<float>(c) * q : 0.f;
+    }
+#pragma unroll
+    for (int o = 1; o < kFinCols; o *= 2) share += __shfl_xor_sync(0xffffffffu, share, o);
+    if (lane == 0) {
+      a.share[i] = n > 0 ? share * __fdiv_rn(a.alpha * E, a.k * nf * nf) : 0.f;
+      if (slab == 0) a.tokens[s] = n;
+    }
+  }
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) s_last = atomicAdd(a.done, 1) == static_cast<int>(gridDim.x) - 1;
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  int live = 0, err = 0;
+  for (int s = tid; s < a.S; s += kBalThreads) live += __ldcg(a.tokens + s) > 0;
+  live = __reduce_add_sync(0xffffffffu, live);
+  if (lane == 0) s_n[warp] = live;
+  __syncthreads();
+  live = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) live += s_n[w];
+  for (int s = tid; s < a.S; s += kBalThreads) {
+    const float nf = static_cast<float>(__ldcg(a.tokens + s));
+    a.coef[s] = nf > 0.f ? __fdiv_rn(a.alpha * E, a.k * nf * nf * static_cast<float>(live)) : 0.f;
+  }
+  float sum = 0.f;
+#pragma unroll 4
+  for (long long i = tid; i < tasks; i += kBalThreads) sum += __ldcg(a.share + i);
+  for (int i = tid; i < a.chunks; i += kBalThreads) err |= a.part_err[i];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) s_sum[warp] = sum;
+  const int bad = __syncthreads_or(err & 2), odd = __syncthreads_or(err & 1);
+  if (tid == 0) {
+    float all = 0.f;
+    for (int w = 0; w < WARPS; ++w) all += s_sum[w];
+    *a.loss = live > 0 ? __fdiv_rn(all, static_cast<float>(live)) : 0.f;
+    *a.status = bad ? MOE_ERR_BAD_OFFSETS : odd ? MOE_ERR_INVALID : MOE_OK;
+  }
 }
 
 // Both passes of a small batch in one launch, the cluster's CTAs a chunk each.
@@ -402,7 +494,7 @@ __global__ void __launch_bounds__(kBalThreads) __cluster_dims__(kFinCluster, 1, 
   extern __shared__ float s_mem[];
   if (static_cast<int>(blockIdx.x) < a.chunks) balance_partial<T, V>(a, s_mem);
   cluster_barrier();   // the partial sums are there, in global memory
-  balance_finish<kBalThreads>(a, cols, w);
+  balance_finish(a, cols, w);
 }
 
 struct RouterGradArgs {
@@ -614,7 +706,9 @@ int launch_grad_to(const RouterGradArgs& a, int out_dtype, int V, int grid, cuda
 size_t balance_workspace_bytes(int T, int E, int S) {
   const size_t chunks = T > 0 ? (T + balance_chunk(T) - 1) / balance_chunk(T) : 0;
   const size_t slots = chunks + S;
-  return 256 + align_up(slots * E * 4, 256) * 2 + align_up(slots * 4, 256) + align_up(chunks * 4 + 4, 256);
+  const size_t tasks = T > kBalSmall ? static_cast<size_t>(S) * ((E + kFinCols - 1) / kFinCols) + S : 0;
+  return 256 + align_up(slots * E * 4, 256) * 2 + align_up(slots * 4, 256) + align_up(chunks * 4 + 4, 256) +
+         align_up(tasks * 4, 256);
 }
 
 int launch_balance_loss(const void* logits, int dtype, const int32_t* idx, int T, int E, int k, const int32_t* off,
@@ -634,19 +728,25 @@ int launch_balance_loss(const void* logits, int dtype, const int32_t* idx, int T
   a.part_c = reinterpret_cast<int32_t*>(p + 256 + m);
   a.part_n = reinterpret_cast<int32_t*>(p + 256 + 2 * m);
   a.part_err = reinterpret_cast<int32_t*>(p + 256 + 2 * m + align_up(slots * 4, 256));
+  a.done = a.status + 1;
+  a.share = reinterpret_cast<float*>(reinterpret_cast<char*>(a.part_err) + align_up(static_cast<size_t>(a.chunks) * 4 + 4, 256));
+  a.tokens = reinterpret_cast<int32_t*>(a.share) + static_cast<size_t>(S) * ((E + kFinCols - 1) / kFinCols);
   a.loss = loss, a.counts = counts, a.prob = prob, a.coef = coef;
-  // columns of a CTA and threads of a column, powers of two: a thread sums
-  // eight slots of a sequence, on average, with their loads in flight together
-  const int threads = T <= kBalSmall ? kBalThreads : kFinThreads;
+  // a small batch: columns of a CTA and threads of a column, powers of two
   int cols = 8;
   while (cols * kFinCluster < E) cols *= 2;
   int w = 1;
-  while (w < 32 && w * cols < threads && w * 8 < a.chunks / S + 1) w *= 2;
+  while (w < 32 && w * cols < kBalThreads && w * 8 < a.chunks / S + 1) w *= 2;
   const int st = dtype == MOE_F32   ? launch_partial<float>(a, V, cols, w, s)
                  : dtype == MOE_F16 ? launch_partial<__half>(a, V, cols, w, s)
                                     : launch_partial<__nv_bfloat16>(a, V, cols, w, s);
   if (st != MOE_OK || T <= kBalSmall) return st;
-  return launch_pdl(__func__, balance_finish_kernel, dim3(kFinCluster), dim3(kFinThreads), 0, s, a, cols, w);
+  // a sequence of more than 16 slots is worth a block's 32 lanes to a column
+  const bool block = a.chunks / S > 16;
+  const long long tasks = static_cast<long long>(S) * ((E + kFinCols - 1) / kFinCols), blocks = block ? tasks : (tasks + 7) / 8;
+  const dim3 grid(static_cast<unsigned>(blocks < 8 * num_sms() ? blocks : 8 * num_sms()));
+  return block ? launch_pdl(__func__, balance_finish_kernel<true>, grid, dim3(kBalThreads), 0, s, a)
+               : launch_pdl(__func__, balance_finish_kernel<false>, grid, dim3(kBalThreads), 0, s, a);
 }
 
 int launch_router_backward(const void* logits, int dtype, const int32_t* idx, const float* d_w, int T, int E, int k,

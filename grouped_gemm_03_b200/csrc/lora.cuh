@@ -114,8 +114,8 @@ int launch_cluster(const char* where, void (*kernel)(Params...), dim3 grid, dim3
 }
 
 // ---------------------------------------------------------------- fragments
-// D += A B, m16n8k16, bf16 operands, fp32 sums.  This tensor path is enough
-// here: the adapters' products are bound by the memory their operands come from.
+// D += A B, m16n8k16, bf16 operands, fp32 sums: for tiles of 16 rows, an eighth
+// of what a tcgen05 MMA takes.
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm volatile(
@@ -175,14 +175,6 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t&
   const float ha = __uint_as_float(hi << 16), hb = __uint_as_float(hi & 0xffff0000u);
   split2(isfinite(ha) ? a - ha : 0.f, isfinite(hb) ? b - hb : 0.f, mid, lo);
 }
-__device__ __forceinline__ void split_store(__nv_bfloat16* hi, __nv_bfloat16* lo, float4 v, float s) {
-  uint32_t h0, l0, h1, l1;
-  split2(v.x * s, v.y * s, h0, l0);
-  split2(v.z * s, v.w * s, h1, l1);
-  *reinterpret_cast<uint2*>(hi) = make_uint2(h0, h1);
-  *reinterpret_cast<uint2*>(lo) = make_uint2(l0, l1);
-}
-
 // The A fragments of rows r0 and r1 (g and g + 8 of an m16 tile), K = RP: lane
 // c of the quad holds elements 4c .. 4c+3 of each 16 (RP = 16), or 8c .. 8c+7
 // of each 32 as its share of two k16 steps; load_b_row deals B alike.

@@ -10,7 +10,10 @@
 // A CTA takes a chunk of one adapter's rows and a slice of X's columns and
 // walks it in tiles of 128 rows x 128 columns.  The projection alone has
 // chunks of 128 rows; the slices of a row meet in a cluster, through
-// distributed shared memory and in rank order, so h leaves it complete.  With
+// distributed shared memory and in rank order, so h leaves it complete.  Its
+// tiles take turns in up to eight accumulators, added up at the end: the tensor
+// cores cut off what an fp32 sum cannot hold, and 112 additions into one left
+// 1.8e-6 of h, twice what a matrix product in fp32 leaves.  With
 // the gradient, G stays in TMEM until the chunk ends (one accumulator to 128
 // columns) and P is complete for the slice after each 128 rows; what several
 // CTAs add to (P over slices, G over chunks) is written as fp32 partial sums
@@ -62,7 +65,7 @@ struct StreamCfg {
   static constexpr bool STACK = RP <= 64;
   static constexpr int GCOLS = GRAD ? (STACK ? kTerms * RP : RP) : 0;       // TMEM columns of 128 of X's
   static constexpr int BLOCKS = !GRAD ? 1 : RP <= 16 ? 4 : 2;  // 128-column blocks, at most
-  static constexpr int PBUF = GRAD ? 2 : 1;                                 // projection accumulators
+  static constexpr int PBUF = GRAD ? 2 : RP <= 32 ? 8 : 4;                  // projection accumulators
   static constexpr int PS = RP + 4;                                         // row stride of P in shared memory: spreads the banks
   static constexpr int PCOL = GRAD ? BLOCKS * GCOLS : 0;                    // their first TMEM column
   static constexpr int USED = PCOL + (PROJ ? PBUF * RP : 0);
@@ -302,15 +305,27 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
         for (int j = 0; j < RP / 2; j += 4) *reinterpret_cast<float4*>(s_p + j) = make_float4(0.f, 0.f, 0.f, 0.f);
       } else if (ptx::mbar_wait_warp(&drained, 0, abort_flag, kWaitLimitNs)) {
         ptx::tc_fence_after();
+        const int used = min(blocks, C::PBUF);
 #pragma unroll
         for (int j = 0; j < RP / 2; j += 8) {
-          uint32_t r[8];
+          float v[8] = {};
           __syncwarp();
-          ptx::tmem_ld_32x32b_x8(tmem + lane_base + half * (RP / 2) + j, r);
-          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int q0 = 0; q0 < C::PBUF; q0 += 4) {
+            if (q0 >= used) break;
+            uint32_t r[4][8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)   // what was not accumulated into is not added
+              tmem_ld(tmem + lane_base + (q0 + q) * RP + half * (RP / 2) + j, r[q]);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int u = 0; u < 8; ++u) v[u] += q0 + q < used ? __uint_as_float(r[q][u]) : 0.f;
+          }
 #pragma unroll
           for (int u = 0; u < 8; u += 4)
-            *reinterpret_cast<uint4*>(s_p + j + u) = make_uint4(r[u], r[u + 1], r[u + 2], r[u + 3]);
+            *reinterpret_cast<float4*>(s_p + j + u) = make_float4(v[u], v[u + 1], v[u + 2], v[u + 3]);
         }
       } else {
         give_up();
@@ -379,7 +394,7 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
     bool ok = true;
     int t = 0;
     for (int step = 0; step < steps && blocks > 0 && ok; ++step) {
-      if (want_p && step >= C::PBUF)
+      if (GRAD && want_p && step >= C::PBUF)
         ok = ptx::mbar_wait(&p_free[step % C::PBUF], (step / C::PBUF - 1) & 1, abort_flag, kWaitLimitNs);
       for (int b = 0; b < blocks && ok; ++b, ++t) {
         ok = ptx::mbar_wait(&full[t % S], (t / S) & 1, abort_flag, kWaitLimitNs);
@@ -387,13 +402,13 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
         ptx::tc_fence_after();
         const uint32_t x = ptx::smem_u32(smem + t % S * C::STAGE);
         if (want_p) {
-          const uint32_t d = tmem + C::PCOL + step % C::PBUF * RP;
+          const uint32_t d = tmem + C::PCOL + (GRAD ? step : b) % C::PBUF * RP;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {  // 16 columns at a time
             const uint64_t md =
                 GRAD ? RT::desc(ptx::smem_u32(s_m) + b * C::RANKS + k * 16 * RT::ROW, RT::LEAD)
                      : ptx::sw128_kmajor_desc(x + 2 * kSub + k / 4 * C::MSUB) + k % 4 * 2;
-            ptx::umma_f16(d, ptx::sw128_kmajor_desc(x + k / 4 * kSub) + k % 4 * 2, md, IP, b > 0 || k > 0);
+            ptx::umma_f16(d, ptx::sw128_kmajor_desc(x + k / 4 * kSub) + k % 4 * 2, md, IP, (GRAD ? b > 0 : b >= C::PBUF) || k > 0);
           }
         }
         if (want_g) {
