@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(256) grad_reduce_kernel(const GradReduceArgs p
 // A chunk's sum runs in the tensor cores' accumulator, which cuts off what it
 // cannot hold: past 2048 rows that would stand out beside a matrix product's in
 // fp32 (1.9e-6 of dB at 4096 rows, 0.8e-6 at 1500).
-constexpr int kMaxChunk = 2048;
+constexpr int kMaxChunk = 1024;
 struct Split {
   int chunk, cols;
 };
