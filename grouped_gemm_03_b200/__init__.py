@@ -2,7 +2,9 @@
 
 Argument marshalling only: every function here checks dtypes, allocates the
 output tensors with torch (device memory is PyTorch's job) and calls the C
-entry point of the same name on the current CUDA stream.  All computation
+entry point of the same name on the current CUDA stream (the fine-tuning
+operators through _ops.so, which does the same in compiled code: their
+smallest calls take less time on the GPU than ctypes does on the host).  All computation
 happens in the library's CUDA kernels; there is no fallback path, and a
 missing or unloadable library raises immediately.
 
@@ -317,48 +319,22 @@ def combine(Y, token_to_row, topk_w, has_shared: bool, out_dtype=torch.bfloat16,
     return o
 
 
-_F32, _I32, _BF16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
-_ACT = (torch.bfloat16, torch.float32)
-_LOGITS = (torch.float32, torch.float16, torch.bfloat16)
-_MASK = (torch.uint8, torch.bool)
+_NATIVE = None
 
 
-def _device(t) -> int:
-    """The device of a call's first tensor, which has to be the current one: kernels launch there."""
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError("tensors must be contiguous CUDA tensors")
-    if dev != torch._C._cuda_getDevice():
-        raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{torch._C._cuda_getDevice()}")
-    return dev
-
-
-def _held(dev, t, what: str, dtypes, shape):
-    """The address of a tensor the call reads or writes (None stays None), checked: contiguous, on the call's
-    device, of one of these types and of this shape."""
-    if t is None:
-        return None
-    if t.get_device() != dev or t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
-        if t.get_device() != dev:
-            raise ValueError(f"{what}: every tensor of a call must be a CUDA tensor on one device (cuda:{dev})")
-        if t.dtype not in dtypes:
-            raise TypeError(f"{what}: unsupported dtype {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{what}: shape {tuple(t.shape)} where {tuple(shape)} is wanted")
-        raise ValueError(f"{what}: tensors must be contiguous CUDA tensors")
-    return t.data_ptr()
-
-
-def _workspace(like, ws, nbytes: int):
-    """The caller's workspace, or a new one of this size, beside `like`."""
-    if ws is None:
-        return like.new_empty(max(nbytes, 256), dtype=torch.uint8)
-    if ws.get_device() != like.get_device() or ws.dtype != torch.uint8 or not ws.is_contiguous():
-        raise ValueError("ws: a contiguous uint8 tensor on the call's device is wanted")
-    return ws
-
-
-_stream_of = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+def _native():
+    """The compiled part of the binding, for the operators from here on (raises if it has not been built)."""
+    global _NATIVE
+    if _NATIVE is None:
+        lib()
+        try:
+            from . import _ops as ops
+        except ImportError as e:
+            raise RuntimeError(f"_ops.so is missing or does not load ({e}): build it with "
+                               "`python -m grouped_gemm_03_b200.build`") from e
+        ops.set_check(_check)
+        _NATIVE = ops
+    return _NATIVE
 
 
 def combine_backward(dout, Y, token_to_row, topk_w, has_shared: bool, offsets=None, want_dY: bool = True,
@@ -370,29 +346,8 @@ def combine_backward(dout, Y, token_to_row, topk_w, has_shared: bool, offsets=No
     if stream is not None:
         with torch.cuda.stream(stream):
             return combine_backward(dout, Y, token_to_row, topk_w, has_shared, offsets, want_dY, want_dw, dY)
-    dev = _device(dout)
-    T, k = token_to_row.shape
-    d = dout.shape[1]
-    rows = T * k + T if has_shared else T * k
-    E = 0 if offsets is None else offsets.numel() - 1 - (1 if has_shared else 0)
-    p_dout = _held(dev, dout, "dout", _ACT, (T, d))
-    p_t2r = _held(dev, token_to_row, "token_to_row", _I32, (T, k))
-    p_w = _held(dev, topk_w, "topk_w", _F32, (T, k))
-    p_off = _held(dev, offsets, "offsets", _I32, (E + 1 + (1 if has_shared else 0),))
-    p_Y = _held(dev, Y, "Y", _BF16, (rows, d))
-    if not want_dY:
-        dY = None
-    elif dY is None:
-        if offsets is not None:
-            dY = dout.new_zeros((rows, d), dtype=torch.bfloat16)
-        else:
-            dY = dout.new_empty((rows, d), dtype=torch.bfloat16) if Y is None else torch.empty_like(Y)
-    dw = torch.empty_like(topk_w) if want_dw else None
-    st = lib().moe_combine_backward(p_dout, _TORCH_DT[dout.dtype], p_Y, p_t2r, p_w, p_off, E, has_shared, T, d, k,
-                                    _held(dev, dY, "dY", _BF16, (rows, d)), dw.data_ptr() if want_dw else None,
-                                    _stream_of(dev))
-    _check(st, "moe_combine_backward")
-    return dY, dw
+    return (_NATIVE or _native()).combine_backward(dout, Y, token_to_row, topk_w, has_shared, offsets, want_dY, want_dw,
+                                                   dY)
 
 
 # ---------------------------------------------------------------- training the router
@@ -406,27 +361,7 @@ def balance_loss(logits, topk_idx, alpha: float, seq_offsets=None, mask=None, wa
     if stream is not None:
         with torch.cuda.stream(stream):
             return balance_loss(logits, topk_idx, alpha, seq_offsets, mask, want_prob, ws)
-    dev = _device(logits)
-    T, E = logits.shape
-    k = topk_idx.shape[1]
-    S = 1 if seq_offsets is None else seq_offsets.numel() - 1
-    if S < 1:
-        raise ValueError("seq_offsets: at least two entries are wanted")
-    p_l = _held(dev, logits, "logits", _LOGITS, (T, E))
-    p_i = _held(dev, topk_idx, "topk_idx", _I32, (T, k))
-    p_o = _held(dev, seq_offsets, "seq_offsets", _I32, (S + 1,))
-    p_m = _held(dev, mask, "mask", _MASK, (T,))
-    L = lib()
-    ws = _workspace(logits, ws, L.moe_balance_loss_workspace_size(T, E, S))
-    counts = topk_idx.new_empty((S, E))
-    loss = logits.new_empty(1, dtype=torch.float32)
-    coef = logits.new_empty(S, dtype=torch.float32)
-    prob = logits.new_empty((S, E), dtype=torch.float32) if want_prob else None
-    st = L.moe_balance_loss(p_l, _TORCH_DT[logits.dtype], p_i, T, E, k, p_o, S, p_m, alpha, loss.data_ptr(),
-                            counts.data_ptr(), prob.data_ptr() if want_prob else None, coef.data_ptr(), ws.data_ptr(), ws.numel(),
-                            _stream_of(dev))
-    _check(st, "moe_balance_loss")
-    return loss, counts, prob, coef
+    return (_NATIVE or _native()).balance_loss(logits, topk_idx, alpha, seq_offsets, mask, want_prob, ws)
 
 
 def router_backward(logits, topk_idx, d_topk_w=None, renormalize: bool = False, counts=None, coef=None, d_loss=None,
@@ -439,27 +374,8 @@ def router_backward(logits, topk_idx, d_topk_w=None, renormalize: bool = False, 
         with torch.cuda.stream(stream):
             return router_backward(logits, topk_idx, d_topk_w, renormalize, counts, coef, d_loss, seq_offsets, mask,
                                    out_dtype, out)
-    dev = _device(logits)
-    T, E = logits.shape
-    k = topk_idx.shape[1]
-    S = 1 if seq_offsets is None else seq_offsets.numel() - 1
-    p_l = _held(dev, logits, "logits", _LOGITS, (T, E))
-    p_i = _held(dev, topk_idx, "topk_idx", _I32, (T, k))
-    p_g = _held(dev, d_topk_w, "d_topk_w", _F32, (T, k))
-    p_o = _held(dev, seq_offsets, "seq_offsets", _I32, (S + 1,))
-    p_m = _held(dev, mask, "mask", _MASK, (T,))
-    p_n = _held(dev, counts, "counts", _I32, (S, E))
-    p_c = _held(dev, coef, "coef", _F32, (S,))
-    if d_loss is not None and d_loss.numel() != 1:
-        raise ValueError("d_loss: one value is wanted")
-    p_d = None if d_loss is None else _held(dev, d_loss, "d_loss", _F32, d_loss.shape)
-    if out is None:
-        out = torch.empty_like(logits, dtype=out_dtype)
-    st = lib().moe_router_backward(p_l, _TORCH_DT[logits.dtype], p_i, p_g, T, E, k, renormalize, p_o, S, p_m, p_n, p_c,
-                                   p_d, _held(dev, out, "out", _LOGITS, (T, E)), _TORCH_DT[out.dtype],
-                                   _stream_of(dev))
-    _check(st, "moe_router_backward")
-    return out
+    return (_NATIVE or _native()).router_backward(logits, topk_idx, d_topk_w, renormalize, counts, coef, d_loss,
+                                                  seq_offsets, mask, out_dtype, out)
 
 
 # ---------------------------------------------------------------- adapters
@@ -469,17 +385,7 @@ def adapter_plan(row_adapter, n: int, ws=None, stream=None):
     if stream is not None:
         with torch.cuda.stream(stream):
             return adapter_plan(row_adapter, n, ws)
-    dev = _device(row_adapter)
-    rows = row_adapter.numel()
-    p_r = _held(dev, row_adapter, "row_adapter", _I32, (rows,))
-    L = lib()
-    ws = _workspace(row_adapter, ws, L.moe_adapter_plan_workspace_size(rows, n))
-    offsets = row_adapter.new_empty(max(n, 0) + 1)
-    order = torch.empty_like(row_adapter)
-    st = L.moe_adapter_plan(p_r, rows, n, offsets.data_ptr(), order.data_ptr(), ws.data_ptr(), ws.numel(),
-                            _stream_of(dev))
-    _check(st, "moe_adapter_plan")
-    return offsets, order
+    return (_NATIVE or _native()).adapter_plan(row_adapter, n, ws)
 
 
 def lora(x, A, B, offsets, order, scale=None, base=None, out_dtype=torch.bfloat16, out=None, want_h: bool = False,
@@ -491,30 +397,7 @@ def lora(x, A, B, offsets, order, scale=None, base=None, out_dtype=torch.bfloat1
     if stream is not None:
         with torch.cuda.stream(stream):
             return lora(x, A, B, offsets, order, scale, base, out_dtype, out, want_h, ws)
-    dev = _device(x)
-    rows, d = x.shape
-    n, R, _ = A.shape
-    N = B.shape[1]
-    p_x = _held(dev, x, "x", _BF16, (rows, d))
-    p_A = _held(dev, A, "A", _BF16, (n, R, d))
-    p_B = _held(dev, B, "B", _BF16, (n, N, R))
-    p_off = _held(dev, offsets, "offsets", _I32, (n + 1,))
-    p_ord = _held(dev, order, "order", _I32, (rows,))
-    p_s = _held(dev, scale, "scale", _F32, (n,))
-    if out is None:
-        out = x.new_empty((rows, N), dtype=out_dtype) if base is None else torch.empty_like(base)
-    p_out = _held(dev, out, "out", _ACT, (rows, N))
-    p_base = _held(dev, base, "base", (out.dtype,), (rows, N))
-    h = x.new_empty((rows, R), dtype=torch.float32) if want_h else None
-    L = lib()
-    need = L.moe_lora_workspace_size(rows, n, d, N, R)
-    if need or ws is not None:
-        ws = _workspace(x, ws, need)
-    st = L.moe_lora(p_x, p_A, p_B, p_s, p_off, p_ord, n, rows, d, N, R, p_base, p_out, _TORCH_DT[out.dtype],
-                    h.data_ptr() if want_h else None, None if ws is None else ws.data_ptr(),
-                    0 if ws is None else ws.numel(), _stream_of(dev))
-    _check(st, "moe_lora")
-    return (out, h) if want_h else out
+    return (_NATIVE or _native()).lora(x, A, B, offsets, order, scale, base, out_dtype, out, want_h, ws)
 
 
 def lora_backward(dC, x, h, A, B, offsets, order, scale=None, dx_base=None, want_dx: bool = True,
@@ -527,37 +410,8 @@ def lora_backward(dC, x, h, A, B, offsets, order, scale=None, dx_base=None, want
         with torch.cuda.stream(stream):
             return lora_backward(dC, x, h, A, B, offsets, order, scale, dx_base, want_dx, want_grads, dx_dtype, dx,
                                  grad_dtype, ws)
-    dev = _device(dC)
-    rows, d = x.shape
-    n, R, _ = A.shape
-    N = B.shape[1]
-    p_dC = _held(dev, dC, "dC", _BF16, (rows, N))
-    p_x = _held(dev, x, "x", _BF16, (rows, d))
-    p_h = _held(dev, h, "h", _F32, (rows, R))
-    p_A = _held(dev, A, "A", _BF16, (n, R, d))
-    p_B = _held(dev, B, "B", _BF16, (n, N, R))
-    p_off = _held(dev, offsets, "offsets", _I32, (n + 1,))
-    p_ord = _held(dev, order, "order", _I32, (rows,))
-    p_s = _held(dev, scale, "scale", _F32, (n,))
-    p_dx = p_base = dA = dB = None
-    dt = MOE_BF16
-    if not want_dx:
-        dx = None
-    else:
-        if dx is None:
-            dx = torch.empty_like(x, dtype=dx_dtype) if dx_base is None else torch.empty_like(dx_base)
-        p_dx = _held(dev, dx, "dx", _ACT, (rows, d))
-        p_base = _held(dev, dx_base, "dx_base", (dx.dtype,), (rows, d))
-        dt = _TORCH_DT[dx.dtype]
-    if want_grads:
-        dA, dB = torch.empty_like(A, dtype=grad_dtype), torch.empty_like(B, dtype=grad_dtype)
-    L = lib()
-    ws = _workspace(x, ws, L.moe_lora_backward_workspace_size(rows, n, d, N, R))
-    st = L.moe_lora_backward(p_dC, p_x, p_h, p_A, p_B, p_s, p_off, p_ord, n, rows, d, N, R, p_base, p_dx, dt,
-                             dA.data_ptr() if want_grads else None, dB.data_ptr() if want_grads else None,
-                             _TORCH_DT[grad_dtype], ws.data_ptr(), ws.numel(), _stream_of(dev))
-    _check(st, "moe_lora_backward")
-    return dx, dA, dB
+    return (_NATIVE or _native()).lora_backward(dC, x, h, A, B, offsets, order, scale, dx_base, want_dx, want_grads,
+                                                dx_dtype, dx, grad_dtype, ws)
 
 
 # ---------------------------------------------------------------- FP8 weights

@@ -1,4 +1,5 @@
-"""Build libmoe.so (the C-ABI library) in-tree with nvcc for sm_100a.
+"""Build libmoe.so (the C-ABI library) in-tree with nvcc for sm_100a, and _ops.so
+beside it, the compiled part of the Python binding (g++, PyTorch's headers).
 
     python -m grouped_gemm_03_b200.build [--force] [-v]
 
@@ -14,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -21,6 +23,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
+OPS_SRC = os.path.join(CSRC, "binding", "ops.cpp")
+OPS = os.path.join(HERE, "_ops.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -79,7 +83,31 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    _build_ops(force, verbose)
     return LIB
+
+
+def _build_ops(force: bool, verbose: bool) -> None:
+    header = os.path.join(INCLUDE, "moe.h")
+    if not force and os.path.exists(OPS) and os.path.getmtime(OPS) >= max(map(os.path.getmtime, (OPS_SRC, header))):
+        return
+    import torch
+
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    includes = [os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include"), cuda,
+                INCLUDE, sysconfig.get_paths()["include"]]
+    tmp = OPS + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f"-I{d}" for d in includes), OPS_SRC,
+           "-o", tmp, f"-L{os.path.join(at, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
+           "-ltorch_python", f"-L{HERE}", "-l:libmoe.so", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {os.path.basename(OPS_SRC)}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, OPS)
 
 
 def main(argv=None) -> int:
