@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kBalThreads = 256;
 constexpr int kBalMinChunk = 32;     // tokens of one block, at least
-constexpr int kBalMaxChunks = 592;   // blocks of the first pass: four on each of 148 SMs
+constexpr int kBalMaxChunks = 444;   // blocks of the first pass: three on each of 148 SMs, all at once
 constexpr int kBalSmall = 512;       // tokens up to which one cluster does both passes
 constexpr int kFinCluster = 8;       // CTAs of a small batch's second pass, each a slice of the experts
 
@@ -205,6 +205,25 @@ __device__ void balance_partial(const BalanceArgs& a, float* s_mem) {
   const int l = lane % L, group = tid / L, groups = kBalThreads / L;
   const T* logits = static_cast<const T*>(a.logits);
   const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
+  // The first rows and, of short chunks with few slots, every token's ids and mask are on their way while the
+  // block finds its sequence.
+  Row<T, V> next;
+  bool next_kept = false;
+  auto fetch = [&](int r, int end) {
+    const bool in = r < end;
+    next.load(logits + static_cast<size_t>(in ? r : t0) * E, E, L, l, a.vec, in);
+    next_kept = in && (!a.mask || a.mask[r]);
+  };
+  fetch(t0 + group, t1);
+  constexpr int kAhead = 8;
+  const bool ahead = a.k <= kAhead && a.chunk <= kBalThreads;
+  int ids[kAhead];
+  bool kept = ahead && t0 + tid < t1;
+  if (kept) {
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) ids[j] = j < a.k ? a.idx[static_cast<size_t>(t0 + tid) * a.k + j] : -1;
+    if (a.mask) kept = a.mask[t0 + tid];
+  }
   if (tid == 0) s_err = 0;
   for (int e = tid; e < E; e += kBalThreads) s_c[e] = 0;
   int s = 0;
@@ -218,6 +237,12 @@ __device__ void balance_partial(const BalanceArgs& a, float* s_mem) {
     if (bad) atomicOr(&s_err, 2);
   }
   __syncthreads();
+  auto count = [&](int e) {
+    if (e >= 0 && e < E)
+      atomicAdd(&s_c[e], 1);   // whole numbers: the order does not show
+    else if (e != -1)
+      atomicOr(&s_err, 1);
+  };
   int t = t0;
   while (t < t1 && s < a.S) {
     const int end = a.off ? min(t1, a.off[s + 1]) : t1;
@@ -226,38 +251,37 @@ __device__ void balance_partial(const BalanceArgs& a, float* s_mem) {
       continue;
     }
     const size_t slot = blockIdx.x + static_cast<size_t>(s);
+    int n = 0;
+    if (ahead) {
+      if (kept && t0 + tid >= t && t0 + tid < end) {
+        n = 1;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+          if (j < a.k) count(ids[j]);
+      }
+    } else {
+      for (int r = t + tid; r < end; r += kBalThreads) {
+        if (a.mask && !a.mask[r]) continue;
+        ++n;
+        for (int j = 0; j < a.k; ++j) count(a.idx[static_cast<size_t>(r) * a.k + j]);
+      }
+    }
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
-    // a warp's lanes run the same number of rounds: rows past the end are not live
-    auto counts_for = [&](int r) { return r < end && (!a.mask || a.mask[r]); };
-    Row<T, V> next;
-    bool next_live = counts_for(t + group);
-    next.load(logits + static_cast<size_t>(next_live ? t + group : t) * E, E, L, l, a.vec, next_live);
+    // a warp's lanes run the same number of rounds: rows past the end do not count
+    if (t > t0) fetch(t + group, end);
     for (int b = t; b < end; b += groups) {
       const Row<T, V> row = next;
-      const int r = b + groups + group;
-      next_live = counts_for(r);
-      next.load(logits + static_cast<size_t>(next_live ? r : t) * E, E, L, l, a.vec, next_live);
+      const bool counts = next_kept && b + group < end;
+      if (b + groups < end) fetch(b + groups + group, end);
       float v[V], m, inv;
       row.values(v);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = counts ? v[i] : -INFINITY;   // whatever a token that does not count holds
       softmax_row<V>(v, L, m, inv);
 #pragma unroll
       for (int i = 0; i < V; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
-    }
-    int n = 0;
-    for (int r = t + tid; r < end; r += kBalThreads) {
-      if (!counts_for(r)) continue;
-      ++n;
-      const int32_t* ids = a.idx + static_cast<size_t>(r) * a.k;
-#pragma unroll 4
-      for (int j = 0; j < a.k; ++j) {
-        const int e = ids[j];
-        if (e >= 0 && e < E)
-          atomicAdd(&s_c[e], 1);   // whole numbers: the order does not show
-        else if (e != -1)
-          atomicOr(&s_err, 1);
-      }
     }
     // the warp's rows, then the block's warps, in a fixed order
 #pragma unroll
@@ -308,34 +332,25 @@ __device__ void balance_finish(const BalanceArgs& a, int cols, int w) {
     first = e > b ? b / a.chunk + s : 0;
     last = e > b ? (e - 1) / a.chunk + s + 1 : 0;
   };
-  // sequences that have tokens
-  int live = 0;
-  for (int s0 = 0; s0 < a.S; s0 += NT) {
-    bool some = false;
-    if (s0 + tid < a.S) {
-      int f, e;
-      slots(s0 + tid, f, e);
-      for (; f < e && !some; ++f) some = a.part_n[f] > 0;
-    }
-    live += __syncthreads_count(some);
-  }
   // the w lanes of a (sequence, column) are neighbours: their sums meet by shuffles
   const int g = NT / (cols * w);                            // sequences at once
   const int j = tid % w, col = tid / w % cols, sg = tid / (cols * w);
   const int e = rank * cols + col;
   float share = 0.f;
+  int live = 0;                                             // sequences that have tokens
   for (int s0 = 0; s0 < a.S; s0 += g) {
     const int s = s0 + sg;
-    const bool in = s < a.S && e < E;
     float q = 0.f;
     int c = 0, n = 0;
-    if (in) {
+    if (s < a.S && sg < g) {
       int f, l;
       slots(s, f, l);
 #pragma unroll 8
       for (int i = f + j; i < l; i += w) {
-        q += a.part_q[static_cast<size_t>(i) * E + e];
-        c += a.part_c[static_cast<size_t>(i) * E + e];
+        if (e < E) {
+          q += a.part_q[static_cast<size_t>(i) * E + e];
+          c += a.part_c[static_cast<size_t>(i) * E + e];
+        }
         n += a.part_n[i];
       }
     }
@@ -344,13 +359,21 @@ __device__ void balance_finish(const BalanceArgs& a, int cols, int w) {
       c += __shfl_xor_sync(0xffffffffu, c, o);
       n += __shfl_xor_sync(0xffffffffu, n, o);
     }
-    if (j == 0 && in) {
+    live += __syncthreads_count(j == 0 && col == 0 && n > 0);
+    if (j == 0 && s < a.S && sg < g && e < E) {
       const float nf = static_cast<float>(n);
-      const float k_s = n > 0 ? __fdiv_rn(a.alpha * E, a.k * nf * nf * static_cast<float>(live)) : 0.f;
       a.counts[static_cast<size_t>(s) * E + e] = c;
       if (a.prob) a.prob[static_cast<size_t>(s) * E + e] = n > 0 ? __fdiv_rn(q, nf) : 0.f;
-      if (e == 0) a.coef[s] = k_s;
-      share += k_s * (static_cast<float>(c) * q);
+      if (n > 0) share += static_cast<float>(c) * q * __fdiv_rn(a.alpha * E, a.k * nf * nf);
+    }
+  }
+  if (rank == 0) {
+    for (int s = tid; s < a.S; s += NT) {
+      int f, l, n = 0;
+      slots(s, f, l);
+      for (; f < l; ++f) n += a.part_n[f];
+      const float nf = static_cast<float>(n);
+      a.coef[s] = n > 0 ? __fdiv_rn(a.alpha * E, a.k * nf * nf * static_cast<float>(live)) : 0.f;
     }
   }
   // the block's share of the loss, in a fixed order
@@ -373,14 +396,14 @@ __device__ void balance_finish(const BalanceArgs& a, int cols, int w) {
     if (tid == 0) {
       float all = 0.f;
       for (int r = 0; r < kFinCluster; ++r) all += s_loss[r];
-      *a.loss = all;
+      *a.loss = live > 0 ? __fdiv_rn(all, static_cast<float>(live)) : 0.f;
       *a.status = bad ? MOE_ERR_BAD_OFFSETS : odd ? MOE_ERR_INVALID : MOE_OK;
     }
   }
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(kBalThreads) balance_partial_kernel(const BalanceArgs a) {
+__global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 1) balance_partial_kernel(const BalanceArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   extern __shared__ float s_mem[];
