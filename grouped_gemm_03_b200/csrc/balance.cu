@@ -71,31 +71,38 @@ __device__ __forceinline__ uint32_t minus_inf_bits(__nv_bfloat16) { return 0xff8
 // bytes and E fills whole pieces.
 template <typename T, int V>
 struct Row {
-  uint4 raw[V / piece<T>()];
+  static constexpr int C = piece<T>(), Q = V / C;
+  uint4 raw[Q];
   // -inf past the row's end, and throughout when it is not live
   __device__ __forceinline__ void load(const T* row, int E, int L, int l, bool vec, bool live) {
-    constexpr int C = piece<T>();
-    const uint32_t none = minus_inf_bits(T());
+    clear();
+    if (!live) return;
+    row += l * C;
+    const int left = E - l * C, step = L * C;
+    if (vec) {
 #pragma unroll
-    for (int q = 0; q < V / C; ++q) {
-      const int c = (q * L + l) * C;
-      raw[q] = make_uint4(none, none, none, none);
-      if (vec) {
-        if (live && c < E) raw[q] = *reinterpret_cast<const uint4*>(row + c);
-      } else if (live) {
+      for (int q = 0; q < Q; ++q)
+        if (q * step < left) raw[q] = *reinterpret_cast<const uint4*>(row + q * step);
+    } else {
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
         alignas(16) T v[C];
         *reinterpret_cast<uint4*>(v) = raw[q];
 #pragma unroll
         for (int u = 0; u < C; ++u)
-          if (c + u < E) v[u] = row[c + u];
+          if (q * step + u < left) v[u] = row[q * step + u];
         raw[q] = *reinterpret_cast<const uint4*>(v);
       }
     }
   }
-  __device__ __forceinline__ void values(float (&v)[V]) const {
-    constexpr int C = piece<T>();
+  __device__ __forceinline__ void clear() {
+    const uint32_t none = minus_inf_bits(T());
 #pragma unroll
-    for (int q = 0; q < V / C; ++q) {
+    for (int q = 0; q < Q; ++q) raw[q] = make_uint4(none, none, none, none);
+  }
+  __device__ __forceinline__ void values(float (&v)[V]) const {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
       float f[C];
       unpack(raw[q], f, T());
 #pragma unroll
@@ -121,12 +128,33 @@ __device__ __forceinline__ void store_run(OT* p, const float* v) {
 }
 
 __device__ __forceinline__ float group_max(float v, int L) {
-  for (int o = L >> 1; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2)
+    if (o < L) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 __device__ __forceinline__ float group_sum(float v, int L) {
-  for (int o = L >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2)
+    if (o < L) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// 2^x by the hardware, what would be denormal as 0: with the compiler's own
+// scaling around it the exponentials were a third of the first pass's work.
+__device__ __forceinline__ float exp2_of(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.44269504f;
+// e^(v - m), m a row's maximum.  One multiply-add v log2 e - m log2 e serves a
+// row whose maximum is within kPlain: the rounding of m log2 e is common to the
+// row and falls out of its softmax.  Past it (a row of nothing but the type's
+// lowest value) the products would overflow, and v - m comes first.
+constexpr float kPlain = 1e30f;
+__device__ __forceinline__ float exp_from(float v, float m) {
+  return fabsf(m) < kPlain ? exp2_of(fmaf(v, kLog2e, -m * kLog2e)) : exp2_of((v - m) * kLog2e);
 }
 
 // The numerators e^(v - m) of a row's softmax in place of its values, with the
@@ -141,14 +169,19 @@ __device__ __forceinline__ void softmax_row(float (&v)[V], int L, float& m, floa
   for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
   m = group_max(m, L);
   if (m == -INFINITY) m = 0.f;
-  float z = 0.f;
+  if (__all_sync(0xffffffffu, fabsf(m) < kPlain)) {
+    const float m2 = -m * kLog2e;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    v[i] = __expf(v[i] - m);
-    z += v[i];
+    for (int i = 0; i < V; ++i) v[i] = exp2_of(fmaf(v[i], kLog2e, m2));
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = exp_from(v[i], m);
   }
-  z = group_sum(z, L);
-  inv = z == 0.f ? 0.f : __fdividef(1.f, z);
+  float z[2] = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < V; ++i) z[i & 1] += v[i];
+  const float all = group_sum(z[0] + z[1], L);
+  inv = all == 0.f ? 0.f : __fdividef(1.f, all);
 }
 
 __device__ __forceinline__ void cluster_barrier() {
@@ -272,13 +305,11 @@ __device__ void balance_partial(const BalanceArgs& a, float* s_mem) {
     // a warp's lanes run the same number of rounds: rows past the end do not count
     if (t > t0) fetch(t + group, end);
     for (int b = t; b < end; b += groups) {
-      const Row<T, V> row = next;
-      const bool counts = next_kept && b + group < end;
+      Row<T, V> row = next;
+      if (!(next_kept && b + group < end)) row.clear();   // whatever a token that does not count holds
       if (b + groups < end) fetch(b + groups + group, end);
       float v[V], m, inv;
       row.values(v);
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = counts ? v[i] : -INFINITY;   // whatever a token that does not count holds
       softmax_row<V>(v, L, m, inv);
 #pragma unroll
       for (int i = 0; i < V; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
@@ -474,37 +505,36 @@ __global__ void __launch_bounds__(kBalThreads) balance_finish_kernel(const Balan
       if (slab == 0) a.tokens[s] = n;
     }
   }
-  __threadfence();
   __syncthreads();
-  if (tid == 0) s_last = atomicAdd(a.done, 1) == static_cast<int>(gridDim.x) - 1;
+  if (tid == 0) {
+    __threadfence();   // the block's results, which the barrier has brought here, before its arrival
+    s_last = atomicAdd(a.done, 1) == static_cast<int>(gridDim.x) - 1;
+    __threadfence();
+  }
   __syncthreads();
   if (!s_last) return;
-  __threadfence();
+  float sum = 0.f;
   int live = 0, err = 0;
+#pragma unroll 4
+  for (long long i = tid; i < tasks; i += kBalThreads) sum += __ldcg(a.share + i);
+  for (int i = tid; i < a.chunks; i += kBalThreads) err |= a.part_err[i];
   for (int s = tid; s < a.S; s += kBalThreads) live += __ldcg(a.tokens + s) > 0;
-  live = __reduce_add_sync(0xffffffffu, live);
-  if (lane == 0) s_n[warp] = live;
-  __syncthreads();
-  live = 0;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) live += s_n[w];
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  live = __reduce_add_sync(0xffffffffu, live);
+  err = __reduce_or_sync(0xffffffffu, err);
+  if (lane == 0) s_sum[warp] = sum, s_n[warp] = live, s_c[warp][0] = err;
+  __syncthreads();
+  sum = 0.f, live = 0, err = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) sum += s_sum[w], live += s_n[w], err |= s_c[w][0];
   for (int s = tid; s < a.S; s += kBalThreads) {
     const float nf = static_cast<float>(__ldcg(a.tokens + s));
     a.coef[s] = nf > 0.f ? __fdiv_rn(a.alpha * E, a.k * nf * nf * static_cast<float>(live)) : 0.f;
   }
-  float sum = 0.f;
-#pragma unroll 4
-  for (long long i = tid; i < tasks; i += kBalThreads) sum += __ldcg(a.share + i);
-  for (int i = tid; i < a.chunks; i += kBalThreads) err |= a.part_err[i];
-#pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) s_sum[warp] = sum;
-  const int bad = __syncthreads_or(err & 2), odd = __syncthreads_or(err & 1);
   if (tid == 0) {
-    float all = 0.f;
-    for (int w = 0; w < WARPS; ++w) all += s_sum[w];
-    *a.loss = live > 0 ? __fdiv_rn(all, static_cast<float>(live)) : 0.f;
-    *a.status = bad ? MOE_ERR_BAD_OFFSETS : odd ? MOE_ERR_INVALID : MOE_OK;
+    *a.loss = live > 0 ? __fdiv_rn(sum, static_cast<float>(live)) : 0.f;
+    *a.status = err & 2 ? MOE_ERR_BAD_OFFSETS : err & 1 ? MOE_ERR_INVALID : MOE_OK;
   }
 }
 
@@ -559,6 +589,7 @@ __global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 1) router_backward_
   for (int i = 0; i < V; ++i) bal[i] = 0.f;
   const float d_loss = a.counts && a.d_loss ? __ldg(a.d_loss) : 1.f;
 
+  const bool two = k > L;   // slots to a lane
   Row<T, V> next;
   int next_e[2] = {-1, -1};
   float next_g[2] = {0.f, 0.f};
@@ -566,11 +597,14 @@ __global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 1) router_backward_
     const bool live = t < t1;
     const size_t tr = live ? t : t0;
     next.load(logits + tr * E, E, L, l, a.vec, live);
+    if (gates) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const bool in = gates && live && l + u * L < k;
-      next_e[u] = in ? __ldg(a.idx + tr * k + l + u * L) : -1;
-      next_g[u] = in ? __ldg(a.d_w + tr * k + l + u * L) : 0.f;
+      for (int u = 0; u < 2; ++u) {
+        if (u && !two) break;
+        const bool in = live && l + u * L < k;
+        next_e[u] = in ? __ldg(a.idx + tr * k + l + u * L) : -1;
+        next_g[u] = in ? __ldg(a.d_w + tr * k + l + u * L) : 0.f;
+      }
     }
   };
   prefetch(t0 + group);
@@ -579,16 +613,20 @@ __global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 1) router_backward_
     const bool live = t < t1;
     const int tr = live ? t : t0;
     const T* row = logits + static_cast<size_t>(tr) * E;
-    float p[V], m, inv;
-    next.values(p);
-    int e[2];
-    float g[2], x[2];
+    Row<T, V> now = next;
+    int e[2] = {-1, -1};
+    float g[2] = {0.f, 0.f}, x[2] = {-INFINITY, -INFINITY};
+    if (gates) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      e[u] = next_e[u] >= 0 && next_e[u] < E ? next_e[u] : -1;
-      g[u] = next_g[u];
-      x[u] = e[u] >= 0 ? to_f32(row[e[u]]) : -INFINITY;
+      for (int u = 0; u < 2; ++u) {
+        if (u && !two) break;
+        e[u] = next_e[u] >= 0 && next_e[u] < E ? next_e[u] : -1;
+        g[u] = e[u] >= 0 ? next_g[u] : 0.f;
+        if (e[u] >= 0) x[u] = to_f32(row[e[u]]);
+      }
     }
+    // a slot without an expert whose gradient is not 0 still makes its row one to work on
+    const bool some = next_g[0] != 0.f || next_g[1] != 0.f;
     if (b + groups < t1) prefetch(t + groups);
     bool in = false;
     if (a.counts) {
@@ -606,21 +644,30 @@ __global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 1) router_backward_
       }
     }
     // something to differentiate: else the row's gradient is 0 whatever its logits hold
-    const bool any = group_max(g[0] != 0.f || g[1] != 0.f ? 1.f : 0.f, L) != 0.f || in;
+    const bool any = group_max(some ? 1.f : 0.f, L) != 0.f || in;
+    if (!any) now.clear();
+    float p[V], m, inv;
+    now.values(p);
     softmax_row<V>(p, L, m, inv);
-    float dot = 0.f;   // sum of p times what it is multiplied with: the loss's part, and the raw gates'
+    float dots[2] = {0.f, 0.f};   // sum of p times what it is multiplied with: the loss's part, and the raw gates'
 #pragma unroll
-    for (int i = 0; i < V; ++i) dot = fmaf(p[i], bal[i], dot);
-    dot = in ? dot * inv : 0.f;
-    float ps[2], z = 0.f, wg = 0.f;
+    for (int i = 0; i < V; ++i) p[i] *= inv;
+    if (in) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      ps[u] = e[u] >= 0 ? __expf(x[u] - m) * inv : 0.f;
-      if (kRenorm) {
-        z += ps[u];
-        wg += e[u] >= 0 ? ps[u] * g[u] : 0.f;
-      } else {
-        dot += e[u] >= 0 ? ps[u] * g[u] : 0.f;
+      for (int i = 0; i < V; ++i) dots[i & 1] = fmaf(p[i], bal[i], dots[i & 1]);
+    }
+    float dot = dots[0] + dots[1];
+    float ps[2] = {0.f, 0.f}, z = 0.f, wg = 0.f;
+    if (gates) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (u && !two) break;
+        ps[u] = e[u] >= 0 && any ? exp_from(x[u], m) * inv : 0.f;
+        const float pg = e[u] >= 0 ? ps[u] * g[u] : 0.f;
+        if (kRenorm)
+          z += ps[u], wg += pg;
+        else
+          dot += pg;
       }
     }
     dot = group_sum(dot, L);
@@ -633,6 +680,7 @@ __global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 1) router_backward_
         const float gj = __shfl_sync(0xffffffffu, j < L ? g[0] : g[1], from);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
+          if (u && !two) break;
           gs[u] += ej == e[u] ? gj : 0.f;
           if (kRenorm) ns[u] += ej == e[u] ? 1.f : 0.f;
         }
@@ -645,29 +693,31 @@ __global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 1) router_backward_
       inv_z = z == 0.f ? 0.f : __fdiv_rn(1.f, z);
       wg *= inv_z;
     }
+    if (in) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) p[i] *= bal[i] - dot;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) p[i] *= -dot;
+    }
     OT* o = out + static_cast<size_t>(tr) * E;
 #pragma unroll
     for (int q = 0; q < V / piece<T>(); ++q) {
       constexpr int C = piece<T>();
       const int c = (q * L + l) * C;
-      float v[C];
-#pragma unroll
-      for (int u = 0; u < C; ++u) {
-        const int i = q * C + u;
-        v[u] = any ? p[i] * inv * ((in ? bal[i] : 0.f) - dot) : 0.f;
-      }
       if (a.vec) {
-        if (live && c < E) store_run<OT, C>(o + c, v);
+        if (live && c < E) store_run<OT, C>(o + c, p + q * C);
       } else {
 #pragma unroll
         for (int u = 0; u < C; ++u)
-          if (live && c + u < E) o[c + u] = from_f32(v[u], OT());
+          if (live && c + u < E) o[c + u] = from_f32(p[q * C + u], OT());
       }
     }
     if (gates) {
       __syncwarp();   // the selected entries come after the row's
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
+        if (u && !two) break;
         if (!live || !any || e[u] < 0) continue;
         const float be = in ? c_s * static_cast<float>(__ldg(a.counts + static_cast<size_t>(s) * E + e[u])) : 0.f;
         float v;
