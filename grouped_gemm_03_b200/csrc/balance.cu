@@ -19,6 +19,8 @@
 // Both kernels are bound by reading the logits (and writing their gradient):
 // one pass, each row held in registers by L lanes of 16 columns (32 past 512
 // experts), the softmax's maximum and sum by shuffles.
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace moe {
@@ -73,12 +75,16 @@ template <typename T, int V>
 struct Row {
   static constexpr int C = piece<T>(), Q = V / C;
   uint4 raw[Q];
-  // -inf past the row's end, and throughout when it is not live
-  __device__ __forceinline__ void load(const T* row, int E, int L, int l, bool vec, bool live) {
-    clear();
-    if (!live) return;
+  // -inf past the row's end; vec = 2: the lanes' pieces are the row
+  __device__ __forceinline__ void load(const T* row, int E, int L, int l, int vec) {
     row += l * C;
     const int left = E - l * C, step = L * C;
+    if (vec == 2) {
+#pragma unroll
+      for (int q = 0; q < Q; ++q) raw[q] = *reinterpret_cast<const uint4*>(row + q * step);
+      return;
+    }
+    clear();
     if (vec) {
 #pragma unroll
       for (int q = 0; q < Q; ++q)
@@ -99,6 +105,22 @@ struct Row {
     const uint32_t none = minus_inf_bits(T());
 #pragma unroll
     for (int q = 0; q < Q; ++q) raw[q] = make_uint4(none, none, none, none);
+  }
+  // the largest value (a NaN is passed over): of 16-bit types two at a time
+  __device__ __forceinline__ float largest() const {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
+    if constexpr (sizeof(T) == 4) {
+      float m = __uint_as_float(w[0]);
+#pragma unroll
+      for (int i = 1; i < 4 * Q; ++i) m = fmaxf(m, __uint_as_float(w[i]));
+      return m;
+    } else {
+      using T2 = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
+      T2 m = *reinterpret_cast<const T2*>(&w[0]);
+#pragma unroll
+      for (int i = 1; i < 4 * Q; ++i) m = __hmax2(m, *reinterpret_cast<const T2*>(&w[i]));
+      return fmaxf(to_f32(m.x), to_f32(m.y));
+    }
   }
   __device__ __forceinline__ void values(float (&v)[V]) const {
 #pragma unroll
@@ -157,17 +179,14 @@ __device__ __forceinline__ float exp_from(float v, float m) {
   return fabsf(m) < kPlain ? exp2_of(fmaf(v, kLog2e, -m * kLog2e)) : exp2_of((v - m) * kLog2e);
 }
 
-// The numerators e^(v - m) of a row's softmax in place of its values, with the
-// row's maximum m and 1 / (their sum).  A logit of -inf has probability 0; a
+// The numerators e^(v - m) of a row's softmax, with the row's maximum m and 1 / (their sum).  A logit of -inf has probability 0; a
 // row of nothing else (a row that is not live is one) has probability 0
 // throughout: inv = 0.  The maximum passes over a NaN, the sum does not, so a
 // NaN logit makes its row NaN.
-template <int V>
-__device__ __forceinline__ void softmax_row(float (&v)[V], int L, float& m, float& inv) {
-  m = v[0];
-#pragma unroll
-  for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
-  m = group_max(m, L);
+template <typename T, int V>
+__device__ __forceinline__ void softmax_row(const Row<T, V>& row, float (&v)[V], int L, float& m, float& inv) {
+  m = group_max(row.largest(), L);
+  row.values(v);
   if (m == -INFINITY) m = 0.f;
   if (__all_sync(0xffffffffu, fabsf(m) < kPlain)) {
     const float m2 = -m * kLog2e;
@@ -230,8 +249,8 @@ template <typename T, int V>
 __device__ void balance_partial(const BalanceArgs& a, float* s_mem) {
   const int E = a.E, L = a.L;
   const int width = L * V;                                    // padded columns
-  float* s_q = s_mem;                                          // [8 warps][width]
-  int* s_c = reinterpret_cast<int*>(s_mem + (kBalThreads / 32) * width);  // [E]
+  float* s_q = s_mem;                                          // [groups][width]
+  int* s_c = reinterpret_cast<int*>(s_mem + kBalThreads * V);   // [E]
   __shared__ int s_err;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (blockIdx.x == 0 && tid == 0) *a.done = 0;
@@ -240,14 +259,16 @@ __device__ void balance_partial(const BalanceArgs& a, float* s_mem) {
   const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
   // The first rows and, of short chunks with few slots, every token's ids and mask are on their way while the
   // block finds its sequence.
-  Row<T, V> next;
-  bool next_kept = false;
-  auto fetch = [&](int r, int end) {
-    const bool in = r < end;
-    next.load(logits + static_cast<size_t>(in ? r : t0) * E, E, L, l, a.vec, in);
-    next_kept = in && (!a.mask || a.mask[r]);
+  int off0 = 0, off1 = 0;
+  if (a.off && tid < a.S) off0 = a.off[tid], off1 = a.off[tid + 1];
+  Row<T, V> row[2];
+  bool row_kept[2];
+  auto fetch = [&](int u, int r, int end) {   // a row past the end, or masked, is loaded and not used
+    const int at = r < end ? r : t0;
+    row[u].load(logits + static_cast<size_t>(at) * E, E, L, l, a.vec);
+    row_kept[u] = r < end && (!a.mask || a.mask[at]);
   };
-  fetch(t0 + group, t1);
+  fetch(0, t0 + group, t1);
   constexpr int kAhead = 8;
   const bool ahead = a.k <= kAhead && a.chunk <= kBalThreads;
   int ids[kAhead];
@@ -259,14 +280,15 @@ __device__ void balance_partial(const BalanceArgs& a, float* s_mem) {
   }
   if (tid == 0) s_err = 0;
   for (int e = tid; e < E; e += kBalThreads) s_c[e] = 0;
-  int s = 0;
+  int s = 0;   // the sequence of token t0: as many as end at or before it
   if (a.off) {
-    // each block checks its share of the offsets
-    const int per = (a.S + a.chunks - 1) / a.chunks;
-    bool bad = blockIdx.x == 0 && tid == 0 && a.off[0] != 0;
-    for (int i = blockIdx.x * per + tid; i < min(a.S, (static_cast<int>(blockIdx.x) + 1) * per); i += kBalThreads)
-      bad |= a.off[i] > a.off[i + 1] || a.off[i + 1] > a.T;
-    s = sequence_at(a.off, a.S, t0);
+    bool bad = tid == 0 && off0 != 0;
+    for (int i0 = 0; i0 < a.S; i0 += kBalThreads) {
+      const int i = i0 + tid;
+      if (i0) off0 = i < a.S ? a.off[i] : 0, off1 = i < a.S ? a.off[i + 1] : 0;
+      bad |= i < a.S && (off0 > off1 || off1 > a.T);
+      s += __syncthreads_count(i < a.S && off1 <= t0);
+    }
     if (bad) atomicOr(&s_err, 2);
   }
   __syncthreads();
@@ -303,35 +325,44 @@ __device__ void balance_partial(const BalanceArgs& a, float* s_mem) {
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
     // a warp's lanes run the same number of rounds: rows past the end do not count
-    if (t > t0) fetch(t + group, end);
-    for (int b = t; b < end; b += groups) {
-      Row<T, V> row = next;
-      if (!(next_kept && b + group < end)) row.clear();   // whatever a token that does not count holds
-      if (b + groups < end) fetch(b + groups + group, end);
+    if (t > t0) fetch(0, t + group, end);
+    auto add = [&](int u, int r) {
+      if (!(row_kept[u] && r < end)) row[u].clear();   // whatever a token that does not count holds
       float v[V], m, inv;
-      row.values(v);
-      softmax_row<V>(v, L, m, inv);
+      softmax_row(row[u], v, L, m, inv);
 #pragma unroll
       for (int i = 0; i < V; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
+    };
+    for (int b = t; b < end; b += 2 * groups) {   // one of the two rows in flight while the other is worked on
+      if (b + groups < end) fetch(1, b + groups + group, end);
+      add(0, b + group);
+      if (b + groups >= end) break;
+      if (b + 2 * groups < end) fetch(0, b + 2 * groups + group, end);
+      add(1, b + groups + group);
     }
-    // the warp's rows, then the block's warps, in a fixed order
+    // the lanes' sums meet in a fixed order: `parts` threads to a column, each some of the groups, then those
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      for (int o = L; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-    if (lane < L) {
-#pragma unroll
-      for (int i = 0; i < V; i += 4)
-        *reinterpret_cast<float4*>(s_q + warp * width + column<T>(i, L, l)) =
-            make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
-    }
+    for (int i = 0; i < V; i += 4)
+      *reinterpret_cast<float4*>(s_q + group * width + column<T>(i, L, l)) =
+          make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
     __shared__ int s_n[kBalThreads / 32];
     n = __reduce_add_sync(0xffffffffu, n);
     if (lane == 0) s_n[warp] = n;
     __syncthreads();
+    const int parts = kBalThreads / width, mine = parts > 1 ? groups / parts : groups;
+    if (parts > 1) {
+      const int e = tid % width, first = tid / width * mine;
+      float q = 0.f;
+#pragma unroll 8
+      for (int g = first; g < first + mine; ++g) q += s_q[g * width + e];
+      __syncthreads();
+      s_q[tid] = q;   // part tid / width of column e
+      __syncthreads();
+    }
     for (int e = tid; e < E; e += kBalThreads) {
       float q = 0.f;
-#pragma unroll
-      for (int w = 0; w < kBalThreads / 32; ++w) q += s_q[w * width + e];
+#pragma unroll 8
+      for (int w = 0; w < (parts > 1 ? parts : groups); ++w) q += s_q[w * width + e];
       a.part_q[slot * E + e] = q;
       a.part_c[slot * E + e] = s_c[e];
       s_c[e] = 0;
@@ -596,7 +627,7 @@ __global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 1) router_backward_
   auto prefetch = [&](int t) {
     const bool live = t < t1;
     const size_t tr = live ? t : t0;
-    next.load(logits + tr * E, E, L, l, a.vec, live);
+    next.load(logits + tr * E, E, L, l, a.vec);   // past the end an earlier row again, not written
     if (gates) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -647,8 +678,7 @@ __global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 1) router_backward_
     const bool any = group_max(some ? 1.f : 0.f, L) != 0.f || in;
     if (!any) now.clear();
     float p[V], m, inv;
-    now.values(p);
-    softmax_row<V>(p, L, m, inv);
+    softmax_row(now, p, L, m, inv);
     float dots[2] = {0.f, 0.f};   // sum of p times what it is multiplied with: the loss's part, and the raw gates'
 #pragma unroll
     for (int i = 0; i < V; ++i) p[i] *= inv;
@@ -746,7 +776,7 @@ int balance_chunk(int T) {
 
 template <typename T>
 int launch_partial(const BalanceArgs& a, int V, int cols, int w, cudaStream_t s) {
-  const size_t smem = (static_cast<size_t>(kBalThreads / 32) * a.L * V + a.E) * 4;
+  const size_t smem = (static_cast<size_t>(kBalThreads) * V + a.E) * 4;
   const dim3 grid(a.chunks), block(kBalThreads);
   if (a.T <= kBalSmall) {
     const dim3 one(kFinCluster);
@@ -793,7 +823,7 @@ int launch_balance_loss(const void* logits, int dtype, const int32_t* idx, int T
   a.chunk = balance_chunk(T);
   a.chunks = T > 0 ? (T + a.chunk - 1) / a.chunk : 0;
   a.L = lanes_for(E, V);
-  a.vec = E % (dtype == MOE_F32 ? 4 : 8) == 0;
+  a.vec = E % (dtype == MOE_F32 ? 4 : 8) != 0 ? 0 : E == a.L * V ? 2 : 1;
   const size_t slots = static_cast<size_t>(a.chunks) + S, m = align_up(slots * E * 4, 256);
   char* p = static_cast<char*>(ws);
   a.status = reinterpret_cast<int*>(p);
@@ -832,7 +862,7 @@ int launch_router_backward(const void* logits, int dtype, const int32_t* idx, co
   a.mask = mask, a.counts = counts, a.coef = coef, a.d_loss = d_loss, a.out = out;
   a.L = lanes_for(E, V);
   while (a.L * 2 < k) a.L *= 2;   // two slots to a lane
-  a.vec = E % (dtype == MOE_F32 ? 4 : 8) == 0;   // then rows of every output type are stored whole too
+  a.vec = E % (dtype == MOE_F32 ? 4 : 8) != 0 ? 0 : E == a.L * V ? 2 : 1;   // not 0: rows of every output type are stored whole too
   const int groups = kBalThreads / a.L;
   const int blocks = num_sms() * 3;   // one wave
   a.chunk = (T + blocks - 1) / blocks;
