@@ -236,8 +236,11 @@ __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __e
 // and every kernel begins with pdl_wait(), which returns once the preceding
 // grid has completed and its memory is visible: no kernel touches global
 // memory before that.  pdl_launch_dependents() lets the next kernel's CTAs
-// be scheduled as soon as every CTA of this grid has issued it.  Both are
-// no-ops for a kernel launched without the attribute.
+// be scheduled as soon as every CTA of this grid has issued it, which each
+// does after its own wait.  Both are no-ops for a kernel launched without the
+// attribute.  A kernel that always follows another one of its own call may
+// read, before it waits, what was there before that other one began: that
+// one's CTAs have all waited when this one starts (the adapters' passes).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

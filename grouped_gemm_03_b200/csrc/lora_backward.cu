@@ -213,7 +213,7 @@ int launch_lora_backward(const LoraBackwardArgs& q, cudaStream_t s) {
   StreamArgs p{};
   p.X = static_cast<const __nv_bfloat16*>(q.dC), p.M = static_cast<const __nv_bfloat16*>(q.B), p.V = image;
   p.scale = q.scale, p.offsets = q.offsets, p.order = q.order, p.n = q.n, p.rows = q.rows, p.W = q.N, p.R = q.R;
-  p.chunk = L.dc.chunk, p.cols = L.dc.cols;
+  p.chunk = L.dc.chunk, p.cols = L.dc.cols, p.early = q.dB != nullptr;
   p.proj = need_dh ? dh_part : nullptr;
   p.part = reinterpret_cast<float*>(ws + L.pB), p.grad = q.dB, p.grad_f32 = q.grad_dtype == MOE_F32;
   p.status = reinterpret_cast<int*>(ws);
@@ -226,7 +226,7 @@ int launch_lora_backward(const LoraBackwardArgs& q, cudaStream_t s) {
   }
   if (q.dA) {
     p.X = static_cast<const __nv_bfloat16*>(q.x), p.M = nullptr, p.W = q.d;
-    p.chunk = L.x.chunk, p.cols = L.x.cols, p.proj = nullptr;
+    p.chunk = L.x.chunk, p.cols = L.x.cols, p.early = true, p.proj = nullptr;
     p.part = reinterpret_cast<float*>(ws + L.pA), p.grad = q.dA;
     st = launch_lora_stream(p, kStreamGrad, s);
     if (st != MOE_OK) return st;

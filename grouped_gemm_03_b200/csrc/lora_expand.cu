@@ -78,10 +78,15 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
     s_abort = 0;
     ptx::fence_mbar_init();
   }
-  pdl_wait();
-  pdl_launch_dependents();
+  // Base, the plan and the weights are older than the launch before this one, which writes h: their loads
+  // start while it runs.
   int a, start, end;
-  if (!find_tile(p.offsets, p.n, p.rows, kRows, blockIdx.x, a, start, end)) return;
+  const bool found = find_tile(p.offsets, p.n, p.rows, kRows, blockIdx.x, a, start, end);
+  if (!found || a == p.n) {
+    pdl_wait();
+    pdl_launch_dependents();
+    if (!found) return;
+  }
   const int N = p.N, R = p.R;
   const int col0 = blockIdx.y * p.cols, col1 = min(N, col0 + p.cols);
   OT* out = static_cast<OT*>(p.out);
@@ -109,14 +114,20 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
   }
   const int blocks = (col1 - col0 + kBC - 1) / kBC;
 
-  if (warp == kMmaWarp) {
-    ptx::tmem_alloc(&s_tmem, 2 * kBC);
-    ptx::tmem_relinquish();
-  }
-  ptx::tc_fence_before();
   __syncthreads();
-  ptx::tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  uint32_t tmem = 0;
+  if (warp >= kLoaders / 32) {   // TMEM only then: as in the streaming pass
+    pdl_wait();
+    if (warp == kMmaWarp) {
+      pdl_launch_dependents();
+      ptx::tmem_alloc(&s_tmem, 2 * kBC);
+      ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    named_barrier(1, kExpandThreads - kLoaders);
+    ptx::tc_fence_after();
+    tmem = s_tmem;
+  }
   auto give_up = [&]() {
     s_abort = 1;
     if (p.status) set_status(p.status, MOE_ERR_TIMEOUT);
@@ -127,17 +138,21 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
     // (l / 8)-th 128 bytes of the block; a row that is not there is taken from behind base, as zeros.
     constexpr int SUBS = kBC * sizeof(OT) / 128;
     const int quad = warp * 8 + lane % 8, sub = lane / 8, quads = (end - start + 3) / 4;  // none behind the last row
-    if (tid == 0) {
-      ptx::mbar_arrive_expect_tx(&h_full, C::H);
-      bulk_load(s_h, p.h + static_cast<size_t>(blockIdx.x) * RankTile<RP>::IMAGE, C::H, &h_full);
-    }
     const uint64_t policy = ptx::policy_evict_first();
     int row[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) row[u] = s_row[quad * 4 + u] >= 0 ? s_row[quad * 4 + u] : p.rows;
     bool ok = true;
     int t = 0;
+    auto load_h = [&]() {
+      if (warp) return;
+      pdl_wait();
+      if (lane) return;
+      ptx::mbar_arrive_expect_tx(&h_full, C::H);
+      bulk_load(s_h, p.h + static_cast<size_t>(blockIdx.x) * RankTile<RP>::IMAGE, C::H, &h_full);
+    };
     for (; t < blocks; ++t) {
+      if (t == S) load_h();   // the ring is full
       if (t >= S && !ptx::mbar_wait_warp(&empty[t % S], (t / S - 1) & 1, abort_flag, kWaitLimitNs)) {
         give_up();
         ok = false;
@@ -160,6 +175,7 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
         gather4_once(dst + sub * (kRows * 128) + quad * 512, &map_base, &full[t % S], col + sub * (128 / sizeof(OT)), row,
                      policy);
     }
+    if (blocks <= S) load_h();
     if (!ok) {   // what is in flight lands before the block ends
       int never = 0;
       for (int u = t > S ? t - S : 0; u < t; ++u) ptx::mbar_wait_warp(&full[u % S], (u / S) & 1, &never, kWaitLimitNs);

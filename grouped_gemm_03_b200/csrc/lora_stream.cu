@@ -143,9 +143,7 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
     s_abort = 0;
     ptx::fence_mbar_init();
   }
-  pdl_wait();
-  pdl_launch_dependents();
-  if (p.status && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *p.status = MOE_OK;
+  if (!p.early) pdl_wait();
   const uint32_t CS = GRAD ? 1 : cluster_size();
   const int slot = GRAD ? blockIdx.x : blockIdx.x / CS, slice = GRAD ? blockIdx.y : cluster_rank();
   int a, start, end;
@@ -154,6 +152,9 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
   const int col0 = slice * p.cols;
   const size_t size = static_cast<size_t>(W) * R;   // G's values of one adapter
   if (!found || a == p.n) {   // the whole cluster leaves
+    pdl_wait();
+    pdl_launch_dependents();
+    if (p.status && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *p.status = MOE_OK;
     if constexpr (GRAD) {     // the slot of an adapter without rows: its gradient is 0
       if (a < p.n && p.grad && held_offset(p.offsets, p.n, p.rows, a) >= held_offset(p.offsets, p.n, p.rows, a + 1)) {
         const size_t first = a * size;
@@ -174,14 +175,23 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
   const int tiles = steps * blocks;
   const bool want_p = PROJ && (!GRAD || p.proj), want_g = GRAD && p.grad;
 
-  if (warp == kMmaWarp) {
-    ptx::tmem_alloc(&s_tmem, C::TMEM);
-    ptx::tmem_relinquish();
-  }
-  ptx::tc_fence_before();
   __syncthreads();
-  ptx::tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  // The loaders go on with what the launch before this one did not write (early); the others wait for its end,
+  // TMEM with them: a block that held some while it waits could keep the ones it waits for from starting.
+  uint32_t tmem = 0;
+  if (warp >= kLoaders / 32) {
+    pdl_wait();
+    if (warp == kMmaWarp) {
+      pdl_launch_dependents();
+      if (p.status && blockIdx.x == 0 && blockIdx.y == 0 && lane == 0) *p.status = MOE_OK;
+      ptx::tmem_alloc(&s_tmem, C::TMEM);
+      ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    named_barrier(1, C::THREADS - kLoaders);
+    ptx::tc_fence_after();
+    tmem = s_tmem;
+  }
   auto give_up = [&]() {
     s_abort = 1;
     if (p.status) set_status(p.status, MOE_ERR_TIMEOUT);
@@ -250,6 +260,7 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
               ++t;
               break;
             }
+            if (step == 0) pdl_wait();
             if (lane == 0)
               bulk_load(s_v + step % VB * C::V_ONE, image + static_cast<size_t>(step) * RT::IMAGE, C::V_ONE, &full[t % S]);
           }

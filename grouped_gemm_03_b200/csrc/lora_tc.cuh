@@ -51,6 +51,10 @@ __device__ __forceinline__ void store32(float* p, const float (&f)[8]) {
                : "memory");
 }
 
+// barrier `id` (not 0) of `threads` threads, whole warps
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
 // byte offset of 16-byte piece `c` (0..7) of row `r` in a tile of 128-byte rows, 128-byte swizzle
 __device__ __forceinline__ uint32_t swz(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
@@ -135,6 +139,8 @@ struct StreamArgs {
   float* part;              // G's partial sums, for the adapters of more than one chunk, by part_slot
   void* grad;               // G: [n, W, R] (dB) or [n, R, W] (dA), 0 for an adapter without rows; nullptr: not wanted
   int grad_f32;
+  bool early;               // the launch before this one in the stream is one of this file's callers' and wrote V alone:
+                            // X, M and the plan are loaded before it ends
   int* status;
 };
 // Adapters of more than one chunk lie part_slot(offset) apart: with m > chunk
