@@ -451,6 +451,7 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
   }
   __syncwarp();
   __syncthreads();
+  if constexpr (!GRAD) cluster_arrive();   // this CTA's slice of P is there
   if (warp == kMmaWarp) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, C::TMEM);
@@ -458,13 +459,18 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
   if constexpr (!GRAD) {
     // CTA `slice` adds up its share of the rows, over the cluster in rank order
     __syncwarp();
-    cluster_arrive();
-    cluster_wait();
     const float sc = p.scale ? __ldg(p.scale + a) : 1.f;
     uint8_t* image = p.image + static_cast<size_t>(slot) * RT::IMAGE;
+    auto row_of = [&](int i) { return i / (RP / 4) * static_cast<int>(CS) + slice; };
+    auto id_of = [&](int i) {
+      return p.h_out && i < kTile / static_cast<int>(CS) * (RP / 4) && start + row_of(i) < end
+                 ? __ldg(p.order + start + row_of(i)) : -1;
+    };
+    int id = id_of(tid);   // in flight across the barrier
+    cluster_wait();
     for (int i = tid; i < kTile / static_cast<int>(CS) * (RP / 4); i += C::THREADS) {
-      const int m = i / (RP / 4) * static_cast<int>(CS) + slice, j = i % (RP / 4) * 4;
-      if (start + m >= end) continue;   // what the image holds there reaches that row of the product alone
+      const int m = row_of(i), j = i % (RP / 4) * 4;
+      if (start + m >= end) break;   // what the image holds there reaches that row of the product alone
       const float4* from = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem) + m * C::PS + j);
       float4 x[8], v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -474,8 +480,8 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
       for (uint32_t q = 0; q < 8; ++q)
         if (q < CS) v.x += x[q].x, v.y += x[q].y, v.z += x[q].z, v.w += x[q].w;
       if (j >= R) v = make_float4(0.f, 0.f, 0.f, 0.f);
-      const int r = p.h_out && j < R ? __ldg(p.order + start + m) : -1;
-      if (r >= 0 && r < p.rows) *reinterpret_cast<float4*>(p.h_out + static_cast<size_t>(r) * R + j) = v;
+      if (j < R && id >= 0 && id < p.rows) *reinterpret_cast<float4*>(p.h_out + static_cast<size_t>(id) * R + j) = v;
+      id = id_of(i + C::THREADS);
       uint32_t w[kTerms][2];
       split3(v.x * sc, v.y * sc, w[0][0], w[1][0], w[2][0]);
       split3(v.z * sc, v.w * sc, w[0][1], w[1][1], w[2][1]);
