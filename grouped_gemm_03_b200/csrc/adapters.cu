@@ -400,7 +400,7 @@ int launch_lora(const LoraForwardArgs& q, cudaStream_t s) {
     StreamArgs p{};
     p.X = static_cast<const __nv_bfloat16*>(q.x), p.M = static_cast<const __nv_bfloat16*>(q.A);
     p.offsets = q.offsets, p.order = q.order, p.n = q.n, p.rows = q.rows, p.W = q.d, p.R = q.R;
-    p.scale = q.scale, p.image = h, p.h_out = q.h_out, p.status = status;
+    p.scale = q.scale, p.image = h, p.h_out = q.h_out, p.status = status, p.first = true;
     // slices of a row: as many as leave two CTAs to an SM, up to the portable cluster
     const long long tiles = (static_cast<long long>(q.rows) + 64ll * q.n) / 128 + 1;  // an adapter's last is half full
     p.chunk = 128, p.cluster = 1;

@@ -216,7 +216,7 @@ int launch_lora_backward(const LoraBackwardArgs& q, cudaStream_t s) {
   p.chunk = L.dc.chunk, p.cols = L.dc.cols, p.early = q.dB != nullptr;
   p.proj = need_dh ? dh_part : nullptr;
   p.part = reinterpret_cast<float*>(ws + L.pB), p.grad = q.dB, p.grad_f32 = q.grad_dtype == MOE_F32;
-  p.status = reinterpret_cast<int*>(ws);
+  p.status = reinterpret_cast<int*>(ws), p.first = true;
   st = launch_lora_stream(p, kStreamBoth, s);
   if (st != MOE_OK) return st;
   if (need_dh) {
@@ -226,7 +226,7 @@ int launch_lora_backward(const LoraBackwardArgs& q, cudaStream_t s) {
   }
   if (q.dA) {
     p.X = static_cast<const __nv_bfloat16*>(q.x), p.M = nullptr, p.W = q.d;
-    p.chunk = L.x.chunk, p.cols = L.x.cols, p.early = true, p.proj = nullptr;
+    p.chunk = L.x.chunk, p.cols = L.x.cols, p.early = true, p.first = false, p.proj = nullptr;
     p.part = reinterpret_cast<float*>(ws + L.pA), p.grad = q.dA;
     st = launch_lora_stream(p, kStreamGrad, s);
     if (st != MOE_OK) return st;

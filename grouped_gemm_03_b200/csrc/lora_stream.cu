@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
   if (!found || a == p.n) {   // the whole cluster leaves
     pdl_wait();
     pdl_launch_dependents();
-    if (p.status && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *p.status = MOE_OK;
+    if (p.first && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *p.status = MOE_OK;
     if constexpr (GRAD) {     // the slot of an adapter without rows: its gradient is 0
       if (a < p.n && p.grad && held_offset(p.offsets, p.n, p.rows, a) >= held_offset(p.offsets, p.n, p.rows, a + 1)) {
         const size_t first = a * size;
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
     pdl_wait();
     if (warp == kMmaWarp) {
       pdl_launch_dependents();
-      if (p.status && blockIdx.x == 0 && blockIdx.y == 0 && lane == 0) *p.status = MOE_OK;
+      if (p.first && blockIdx.x == 0 && blockIdx.y == 0 && lane == 0) *p.status = MOE_OK;
       ptx::tmem_alloc(&s_tmem, C::TMEM);
       ptx::tmem_relinquish();
     }

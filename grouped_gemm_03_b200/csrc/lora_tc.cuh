@@ -141,6 +141,7 @@ struct StreamArgs {
   int grad_f32;
   bool early;               // the launch before this one in the stream is one of this file's callers' and wrote V alone:
                             // X, M and the plan are loaded before it ends
+  bool first;               // of the call's launches that have a status: it starts as MOE_OK
   int* status;
 };
 // Adapters of more than one chunk lie part_slot(offset) apart: with m > chunk
