@@ -11,6 +11,7 @@ namespace moe {
 
 constexpr int kMaxAdapters = 1024;
 constexpr int kMaxRank = 128;
+constexpr int kMaxAdapterCols = 1 << 20;
 
 // Tiles of `rows` rows in adapter order, each of one adapter.  Tile u belongs
 // to the adapter a with the largest base(a) = offsets[a] / MT + a <= u and is

@@ -459,6 +459,7 @@ int check_adapter_shape(int n, int rows, int d, int N, int R) {
   if (n <= 0 || rows < 0 || d <= 0 || N <= 0 || R <= 0) return MOE_ERR_INVALID;
   if (n > kMaxAdapters || rows > kMaxPermuteRows) return MOE_ERR_UNSUPPORTED;
   if (R % 8 != 0 || R > kMaxRank || d % 8 != 0 || N % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  if (d > kMaxAdapterCols || N > kMaxAdapterCols) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 }  // namespace

@@ -397,8 +397,8 @@ int moe_adapter_plan(const int32_t* row_adapter, int rows, int n, int32_t* offse
  *   ws     moe_lora_workspace_size(...) bytes (status + h); where that is 0, NULL
  * fp32 sums, rounded once to out_dtype.  Status word (where there is a
  * workspace): MOE_ERR_TIMEOUT.  R a multiple of 8, 8 <= R <= 128
- * (pad smaller ranks with zeros); d % 8 == 0, N % 8 == 0; x, A, B, base, out
- * and h_out 16-byte aligned; out must not overlap x. */
+ * (pad smaller ranks with zeros); d % 8 == 0, N % 8 == 0, both <= 2^20; x, A, B,
+ * base, out and h_out 16-byte aligned; out must not overlap x. */
 size_t moe_lora_workspace_size(int rows, int n, int d, int N, int R);
 int moe_lora(const void* x, const void* A, const void* B, const float* scale, const int32_t* offsets,
              const int32_t* order, int n, int rows, int d, int N, int R, const void* base, void* out, int out_dtype,

@@ -2,8 +2,9 @@
 
 Tolerances, from the arithmetic: bf16 products are exact in fp32, and a sum of n of them is off by at most
 depth * 2^-23 * (the sum of magnitudes), depth = the additions one result goes through: n / 16 mma steps of
-one warp at most, and 64 for the joins of warps, CTAs and slices.  h and dh enter their products as two bf16
-terms, which leaves 2^-17 of them.  The result is rounded once, half a step of its type.
+one accumulator at most, and 64 for the joins of warps, CTAs and slices.  h and dh enter a product with a bf16 result
+as two bf16 terms, which leaves 2^-17 of them, and as three where the result is fp32.  The result is rounded once, half
+a step of its type.
 """
 import numpy as np
 import pytest
@@ -292,3 +293,69 @@ def test_rows_past_32_bit_offsets():
     out = torch.zeros(rows, N, dtype=torch.bfloat16, device=DEV)
     gg.lora(x, A, B, off, order, base=out, out=out)
     assert (out[-3:] == d * R).all() and not out[:-3].any()
+
+
+# rows around the border between the forward's one launch and two, and adapters of several chunks of a gradient
+@pytest.mark.parametrize("rows,n,d,N,R,only", [(32, 2, 136, 264, 24, None), (33, 2, 136, 264, 24, None),
+                                               (2600, 2, 512, 392, 16, [0]), (2600, 3, 264, 512, 32, [0, 0, 2]),
+                                               (3100, 2, 1160, 648, 64, [1]), (2300, 2, 256, 384, 128, [0, 0, 1])])
+def test_borders(rows, n, d, N, R, only):
+    s = _inputs(rows, n, d, N, R, seed=rows + R, only=only)
+    x, A, B, scale, base, dC, dx_base = _gpu(s, "x", "A", "B", "scale", "base", "dC", "dx_base")
+    off, order = _plan(s, n)
+    out, h = gg.lora(x, A, B, off, order, scale=scale, base=base.float(), want_h=True)
+    _check_forward(s, out, h, s["scale"], s["base"].float())
+    got = gg.lora_backward(dC, x, h, A, B, off, order, scale=scale, dx_base=dx_base)
+    _check_backward(s, got, h.cpu(), s["scale"], s["dx_base"])
+
+
+def test_what_a_workspace_holds_does_not_show():
+    rows, n, d, N, R = 700, 5, 264, 392, 40
+    s = _inputs(rows, n, d, N, R, seed=11)
+    x, A, B, dC = _gpu(s, "x", "A", "B", "dC")
+    off, order = _plan(s, n)
+    L = gg.lib()
+    f = torch.empty(L.moe_lora_workspace_size(rows, n, d, N, R), dtype=torch.uint8, device=DEV)
+    b = torch.empty(L.moe_lora_backward_workspace_size(rows, n, d, N, R), dtype=torch.uint8, device=DEV)
+    h = torch.randn(rows, R, device=DEV)
+    got = []
+    for fill in (0, 0x7f, 0xff):   # zeros, large values, NaNs
+        f.fill_(fill)
+        b.fill_(fill)
+        got.append((*gg.lora(x, A, B, off, order, want_h=True, ws=f), *gg.lora_backward(dC, x, h, A, B, off, order, ws=b)))
+        assert gg.read_device_status(f) == 0 and gg.read_device_status(b) == 0
+    for other in got[1:]:
+        assert all(torch.equal(u, v) for u, v in zip(got[0], other))
+
+
+@pytest.mark.parametrize("rows", [30, 400])
+def test_another_adapters_values_stay_its_own(rows):
+    # weights, rows and gradients that are not finite reach nothing of another adapter, whichever lies beside it
+    n, d, N, R = 3, 136, 72, 24
+    s = _inputs(rows, n, d, N, R, seed=12, bare=False)
+    row = torch.from_numpy(s["row"]).to(DEV)
+    x, A, B, dC = _gpu(s, "x", "A", "B", "dC")
+    off, order = _plan(s, n)
+    h = torch.randn(rows, R, device=DEV)
+    good = (gg.lora(x, A, B, off, order), *gg.lora_backward(dC, x, h, A, B, off, order))
+    mine = row == 1
+    x[mine], dC[mine], h[mine] = float("nan"), float("inf"), float("nan")
+    A[1], B[1] = float("nan"), float("inf")
+    bad = (gg.lora(x, A, B, off, order), *gg.lora_backward(dC, x, h, A, B, off, order))
+    for g, b, per_row in zip(good, bad, (True, True, False, False)):
+        keep = ~mine if per_row else torch.tensor([True, False, True], device=DEV)
+        assert torch.equal(g[keep], b[keep]) and not torch.isfinite(b[~keep]).any()
+
+
+def test_gradients_past_32_bit_offsets():
+    rows, N, d, R = 300000, 7168, 8, 8
+    dC = torch.zeros(rows, N, dtype=torch.bfloat16, device=DEV)
+    dC[-3:] = 1
+    x = torch.ones(rows, d, dtype=torch.bfloat16, device=DEV)
+    A = torch.ones(1, R, d, dtype=torch.bfloat16, device=DEV)
+    B = torch.ones(1, N, R, dtype=torch.bfloat16, device=DEV)
+    row = torch.full((rows,), -1, dtype=torch.int32, device=DEV)
+    row[-3:] = 0
+    off, order = gg.adapter_plan(row, 1)
+    dx, dA, dB = gg.lora_backward(dC, x, torch.full((rows, R), 2.0, device=DEV), A, B, off, order, dx_dtype=torch.float32)
+    assert (dx[-3:] == N * R).all() and not dx[:-3].any() and (dA == 3 * N).all() and (dB == 6).all()

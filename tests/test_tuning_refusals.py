@@ -66,6 +66,7 @@ def test_lora(L):
     for R in (4, 12, 136):
         assert _lora(L, R=R) == UNSUPPORTED
     assert _lora(L, R=0) == INVALID and _lora(L, d=68) == UNSUPPORTED and _lora(L, N=60) == UNSUPPORTED
+    assert _lora(L, d=(1 << 20) + 8) == UNSUPPORTED and _lora(L, N=(1 << 20) + 8) == UNSUPPORTED
     assert _lora(L, n=0) == INVALID and _lora(L, n=1025) == UNSUPPORTED and _lora(L, rows=-1) == INVALID
     assert _lora(L, dt=1) == INVALID and _lora(L, out=P) == INVALID      # out must not be x
     for name in ("x", "A", "B", "off", "order", "out"):
@@ -116,3 +117,12 @@ def test_binding_refuses_host_tensors():
     b = torch.zeros(4, 8, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
         gg.lora(b, b[None], b[None], i[:, 0], i[:, 0])
+
+
+def test_binding_refuses_what_is_no_tensor():
+    with pytest.raises(TypeError, match="logits"):
+        gg.balance_loss([1.0], torch.zeros(4, 2, dtype=torch.int32), 0.1)
+    with pytest.raises(TypeError, match="row_adapter"):
+        gg.adapter_plan(None, 2)
+    with pytest.raises(TypeError):
+        gg.lora(1, 2, 3, 4, 5)
