@@ -170,7 +170,7 @@ struct LoraTile {
 };
 
 template <int RP, typename OT>
-__global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraArgs p) {
+__global__ void __launch_bounds__(kLoraThreads, RP <= 64 ? 2 : 1) lora_kernel(const LoraArgs p) {
   constexpr int TERMS = sizeof(OT) == 4 ? 3 : 2;
   using L = LoraTile<RP, TERMS>;
   constexpr int HS = L::HS;
@@ -213,6 +213,36 @@ __global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraArgs p) {
     return;
   }
 
+  // What the second product takes from memory for a warp's 32 columns, of the first ones on its way while h is
+  // formed (up to rank 32: above, the registers go to h).
+  constexpr bool kAhead = RP <= 32;
+  const int nb0 = n0 + warp * 32;
+  size_t ro[2];
+  bool rl[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = s_row[g + 8 * h];
+    rl[h] = r >= 0;
+    ro[h] = static_cast<size_t>(r >= 0 ? r : 0) * p.N + c * 8;
+  }
+  // the mma's n index g of block t is column (g / 2) * 8 + 2 t + g % 2 of 32
+  const __nv_bfloat16* Bc = p.B + (static_cast<size_t>(a) * p.N + (g >> 1) * 8 + (g & 1)) * p.R;
+  float v[2][8];
+  uint32_t bw[4][RP / 16][2];
+  auto fetch = [&](int nb) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[h][i] = 0.f;
+      if (base && nb + c * 8 < n1 && rl[h]) load8(base + ro[h] + nb, v[h]);
+    }
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        load_b_row<RP>(Bc + static_cast<size_t>(nb + 2 * t) * p.R, nb + (g >> 1) * 8 < n1, p.R, c, bw[t]);
+    }
+  };
+
   // ---- h over this CTA's columns of x
   {
     float acc[RP / 8][4];
@@ -250,6 +280,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraArgs p) {
           mma16816(acc[j], xv[u][0].z, xv[u][1].z, xv[u][0].w, xv[u][1].w, av[u][j].z, av[u][j].w);
         }
     }
+    fetch(nb0);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float* o = s_red + (static_cast<size_t>(warp) * MT + g + 8 * h) * RP + 2 * c;
@@ -293,44 +324,36 @@ __global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraArgs p) {
   uint32_t hf[TERMS][RP / 16][4];
 #pragma unroll
   for (int q = 0; q < TERMS; ++q) load_terms<RP>(s_h + (q * MT + g) * HS, s_h + (q * MT + g + 8) * HS, c, hf[q]);
-  size_t ro[2];
-  bool rl[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = s_row[g + 8 * h];
-    rl[h] = r >= 0;
-    ro[h] = static_cast<size_t>(r >= 0 ? r : 0) * p.N + c * 8;
-  }
-  // the mma's n index g of block t is column (g / 2) * 8 + 2 t + g % 2 of 32
-  const __nv_bfloat16* Bc = p.B + (static_cast<size_t>(a) * p.N + (g >> 1) * 8 + (g & 1)) * p.R;
-  for (int nb = n0 + warp * 32; nb < n1; nb += WK * 32) {
-    float acc[4][4];
+  for (int nb = nb0; nb < n1; nb += WK * 32) {
+    if (nb != nb0) fetch(nb);
     const bool in = nb + c * 8 < n1;
+    float acc[4][4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[8] = {};
-      if (base && in && rl[h]) load8(base + ro[h] + nb, v);
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) acc[t][2 * h] = v[2 * t], acc[t][2 * h + 1] = v[2 * t + 1];
-    }
-    const bool bin = nb + (g >> 1) * 8 < n1;
+      for (int t = 0; t < 4; ++t) acc[t][2 * h] = v[h][2 * t], acc[t][2 * h + 1] = v[h][2 * t + 1];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      uint32_t b[RP / 16][2];
-      load_b_row<RP>(Bc + static_cast<size_t>(nb + 2 * t) * p.R, bin, p.R, c, b);
+      uint32_t bt[RP / 16][2];
+      if constexpr (kAhead) {
+#pragma unroll
+        for (int k = 0; k < RP / 16; ++k) bt[k][0] = bw[t][k][0], bt[k][1] = bw[t][k][1];
+      } else {
+        load_b_row<RP>(Bc + static_cast<size_t>(nb + 2 * t) * p.R, nb + (g >> 1) * 8 < n1, p.R, c, bt);
+      }
 #pragma unroll
       for (int k = 0; k < RP / 16; ++k)
 #pragma unroll
         for (int q = TERMS - 1; q >= 0; --q)   // the small terms first
-          mma16816(acc[t], hf[q][k][0], hf[q][k][1], hf[q][k][2], hf[q][k][3], b[k][0], b[k][1]);
+          mma16816(acc[t], hf[q][k][0], hf[q][k][1], hf[q][k][2], hf[q][k][3], bt[k][0], bt[k][1]);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (!in || !rl[h]) continue;
-      float v[8];
+      float o[8];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) v[2 * t] = acc[t][2 * h], v[2 * t + 1] = acc[t][2 * h + 1];
-      store8(out + ro[h] + nb, v);
+      for (int t = 0; t < 4; ++t) o[2 * t] = acc[t][2 * h], o[2 * t + 1] = acc[t][2 * h + 1];
+      store8(out + ro[h] + nb, o);
     }
   }
   cluster_wait();
@@ -343,11 +366,12 @@ int launch_lora_tiles(LoraArgs& p, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   const int st = allow_smem(done, kernel, L::SMEM);
   if (st != MOE_OK) return st;
-  // CTAs to fill the SMs twice, each with at least 128 columns of the wider side
-  const long long tiles = static_cast<long long>(p.rows) / MT + p.n;
+  // as many CTAs as are resident together, two to an SM up to rank 64 (a second wave took 11.3 us where one takes
+  // 6.8: 61 rows of 48 adapters, clusters of 8 against 4), each with at least 128 columns of the wider side
+  const long long tiles = static_cast<long long>(p.rows) / MT + p.n, room = (RP <= 64 ? 2ll : 1ll) * num_sms();
   const int widest = p.d > p.N ? p.d : p.N;
   int cs = 1;
-  while (cs < 8 && tiles * cs < 4ll * num_sms() && widest >= cs * 2 * 128) cs *= 2;
+  while (cs < 8 && 2 * tiles * cs <= room && widest >= cs * 2 * 128) cs *= 2;
   p.kslice = ((p.d + cs - 1) / cs + 31) / 32 * 32;
   p.nslice = ((p.N + cs - 1) / cs + 31) / 32 * 32;
   return launch_cluster("lora_kernel", kernel, dim3(static_cast<unsigned>(tile_slots<MT>(p.rows, p.n) * cs)),
