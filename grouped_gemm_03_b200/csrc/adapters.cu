@@ -3,8 +3,8 @@
 //   out[r] = base[r] + s_a (x[r] A_a^T) B_a^T,   a = the row's adapter.
 // A_a is [R, d], B_a [N, R] (both K-major like the library's weights).
 //
-// Forward.  Up to 16 rows to an adapter (decode: a token or so to a request) one
-// launch does it: a tile is up to 16 rows of one adapter, a cluster of up to
+// Forward.  While an adapter's weights are not read too often that way (decode, a
+// token or so to a request; mixed steps) one launch does it: a tile is up to 16 rows of one adapter, a cluster of up to
 // eight CTAs shares it.  CTA q multiplies the q-th slice of x's columns with
 // A_a, the cluster's partial x A^T meet through distributed shared memory in
 // rank order, and CTA q then adds its slice of the N output columns.  x, base
@@ -16,8 +16,8 @@
 // dealt to the mma's n index so that a lane holds 8 consecutive ones.  No
 // shared-memory staging, full sectors both ways.
 //
-// With more rows the two products are launches of their own on tiles of 128
-// rows (lora_stream.cu, lora_expand.cu).
+// Else the two products are launches of their own on tiles of 128 rows
+// (lora_stream.cu, lora_expand.cu).
 //
 // h enters the second product as two bf16 terms (hi + lo, 16 bits of mantissa
 // together) for a bf16 result and as three (all 24) for an fp32 one: one bf16
@@ -368,7 +368,8 @@ int launch_lora_tiles(LoraArgs& p, cudaStream_t s) {
   if (st != MOE_OK) return st;
   // as many CTAs as are resident together, two to an SM up to rank 64 (a second wave took 11.3 us where one takes
   // 6.8: 61 rows of 48 adapters, clusters of 8 against 4), each with at least 128 columns of the wider side
-  const long long tiles = static_cast<long long>(p.rows) / MT + p.n, room = (RP <= 64 ? 2ll : 1ll) * num_sms();
+  const long long half_full = p.rows / MT + p.n / 2, one_each = p.n < p.rows ? p.n : p.rows;
+  const long long tiles = half_full > one_each ? half_full : one_each, room = (RP <= 64 ? 2ll : 1ll) * num_sms();
   const int widest = p.d > p.N ? p.d : p.N;
   int cs = 1;
   while (cs < 8 && 2 * tiles * cs <= room && widest >= cs * 2 * 128) cs *= 2;
@@ -409,16 +410,32 @@ int launch_adapter_plan(const int32_t* adapter, int rows, int n, int32_t* offset
                     static_cast<const int32_t*>(cnt), static_cast<const int32_t*>(err), offsets, order, status);
 }
 
-// More than one 16-row tile to an adapter
-bool lora_two_launches(int rows, int n) { return rows > 16ll * n; }
+// Whether the forward's products are launches of their own, by an estimate of
+// both ways' times from what they move.  One launch reads an adapter's weights
+// for every 16 of its rows, out of L2 (at 8 TB/s; at 4 above rank 64, where one
+// CTA fills an SM), two launches read them for every 128, but start twice and
+// leave the last 128 rows of each adapter in part empty.  Measured, one launch
+// against two, columns 4096 and 4096 where not given:
+//   rank 16:  1024 rows of 8 adapters 10.0 / 18.3 us, 4096 of 1 30.8 / 30.2, 8192 of 1 57.5 / 48.2,
+//             8192 of 128 61.5 / 72.7
+//   rank 32:  4096 of 16 35.2 / 44.2, 8192 of 8 (7168 columns in) 79.9 / 59.8
+//   rank 64:  256 of 8 12.8 / 15.4, 2048 of 4 27.6 / 29.0, 4096 of 4 47.3 / 34.7, 8192 of 32 92.8 / 61.5
+//   rank 128: 256 of 4 16.3 / 15.8, 1024 of 16 52.6 / 36.2
+bool lora_two_launches(int rows, int n, int d, int N, int R) {
+  const double ns_per_hbm_byte = 1 / 6400.0, row = 2.0 * d + 4.0 * N, weights = 2.0 * R * (d + N);
+  const double active = n < rows ? n : rows, tiles = rows / 16.0 + 0.5 * active;
+  const double one = 4500 + (rows * row + active * weights) * ns_per_hbm_byte + tiles * weights / (R <= 64 ? 8000 : 4000);
+  const double two = 9500 + 40.0 * R + ((rows + 32.0 * active) * row + active * weights) / 5000;
+  return two < one;
+}
 
-size_t lora_workspace_bytes(int rows, int n, int R) {
-  return lora_two_launches(rows, n) ? 256 + image_bytes(rows, n, R) : 0;
+size_t lora_workspace_bytes(int rows, int n, int d, int N, int R) {
+  return lora_two_launches(rows, n, d, N, R) ? 256 + image_bytes(rows, n, R) : 0;
 }
 
 int launch_lora(const LoraForwardArgs& q, cudaStream_t s) {
   if (q.rows == 0) return MOE_OK;
-  if (lora_two_launches(q.rows, q.n)) {
+  if (lora_two_launches(q.rows, q.n, q.d, q.N, q.R)) {
     int* status = static_cast<int*>(q.ws);
     uint8_t* h = static_cast<uint8_t*>(q.ws) + 256;
     StreamArgs p{};

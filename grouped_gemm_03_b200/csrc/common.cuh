@@ -187,7 +187,7 @@ struct LoraForwardArgs {
   float* h_out;
   void* ws;
 };
-size_t lora_workspace_bytes(int rows, int n, int R);
+size_t lora_workspace_bytes(int rows, int n, int d, int N, int R);
 int launch_lora(const LoraForwardArgs& a, cudaStream_t s);
 struct LoraBackwardArgs {
   const void* dC;

@@ -481,7 +481,7 @@ int moe_adapter_plan(const int32_t* row_adapter, int rows, int n, int32_t* offse
 
 size_t moe_lora_workspace_size(int rows, int n, int d, int N, int R) {
   if (check_adapter_shape(n, rows, d, N, R) != MOE_OK) return 0;
-  return lora_workspace_bytes(rows, n, R);
+  return lora_workspace_bytes(rows, n, d, N, R);
 }
 
 int moe_lora(const void* x, const void* A, const void* B, const float* scale, const int32_t* offsets,
@@ -495,7 +495,7 @@ int moe_lora(const void* x, const void* A, const void* B, const float* scale, co
   if (!aligned(x, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(base, 16) || !aligned(out, 16) ||
       !aligned(h_out, 16))
     return MOE_ERR_INVALID;
-  const size_t need = lora_workspace_bytes(rows, n, R);
+  const size_t need = lora_workspace_bytes(rows, n, d, N, R);
   if (need > 0 && (!ws || !aligned(ws, 256) || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   LoraForwardArgs a{};
   a.x = x, a.A = A, a.B = B, a.scale = scale, a.offsets = offsets, a.order = order;

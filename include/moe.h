@@ -384,8 +384,8 @@ int moe_adapter_plan(const int32_t* row_adapter, int rows, int n, int32_t* offse
                      size_t ws_bytes, void* stream);
 
 /* out[r] = base[r] + scale[a] * (x[r] A[a]^T) B[a]^T for the rows of adapter a,
- * out[r] = base[r] for the rows without one; one launch for a few rows to an
- * adapter, two on the tensor cores for more.
+ * out[r] = base[r] for the rows without one; one launch, or two where an
+ * adapter has rows enough for them (an estimate from the sizes decides).
  *   x      [rows, d] MOE_BF16;  A [n, R, d], B [n, N, R] MOE_BF16;  scale [n] fp32 or NULL (1)
  *   offsets, order  the plan (DEVICE arrays; entries outside their range are
  *          skipped, nothing outside the buffers is read or written)

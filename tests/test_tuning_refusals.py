@@ -73,11 +73,12 @@ def test_lora(L):
         assert _lora(L, **{name: NULL}) == INVALID
     for name in ("x", "A", "B", "base", "out"):
         assert _lora(L, **{name: ODD}) == INVALID
-    need = L.moe_lora_workspace_size(1000, 2, 64, 64, 8)
+    big = dict(rows=8192, n=2, d=7168, N=4096, R=32)   # two launches, with h between them
+    need = L.moe_lora_workspace_size(8192, 2, 7168, 4096, 32)
     assert need > 0 and L.moe_lora_workspace_size(10, 2, 64, 64, 8) == 0
-    assert L.moe_lora_workspace_size(1000, 2, 64, 64, 20) == 0
-    assert _lora(L, rows=1000) == WORKSPACE and _lora(L, rows=1000, ws=P, nb=need - 1) == WORKSPACE
-    assert _lora(L, rows=1000, ws=ODD, nb=BIG) == WORKSPACE
+    assert L.moe_lora_workspace_size(8192, 2, 7168, 4096, 20) == 0
+    assert _lora(L, **big) == WORKSPACE and _lora(L, ws=P, nb=need - 1, **big) == WORKSPACE
+    assert _lora(L, ws=ODD, nb=BIG, **big) == WORKSPACE
 
 
 def _back(L, dC=P, x=P, h=P, n=2, rows=10, d=64, N=64, R=8, dx=Q, dxt=2, dA=Q, dB=Q, gt=0, ws=P, nb=BIG):
