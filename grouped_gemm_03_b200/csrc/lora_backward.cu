@@ -248,8 +248,8 @@ int launch_lora_backward(const LoraBackwardArgs& q, cudaStream_t s) {
   r.size[0] = sizeA, r.size[1] = sizeB;
   r.chunk[0] = L.x.chunk, r.chunk[1] = L.dc.chunk;
   r.offsets = q.offsets, r.n = q.n, r.rows = q.rows;
-  // eight blocks to an SM over all the adapters, no more than one pass needs
-  const size_t need = (r.size[0] > r.size[1] ? r.size[0] : r.size[1]) / 1024 + 1, share = 8ul * num_sms() / q.n + 1;
+  // four blocks to an SM over all the adapters, no more than one pass needs
+  const size_t need = (r.size[0] > r.size[1] ? r.size[0] : r.size[1]) / 1024 + 1, share = 4ul * num_sms() / q.n + 1;
   const dim3 grid(static_cast<unsigned>(need < share ? need : share), q.n, 2);
   return launch_pdl("grad_reduce_kernel", q.grad_dtype == MOE_F32 ? grad_reduce_kernel<float> : grad_reduce_kernel<__nv_bfloat16>,
                     grid, dim3(256), 0, s, r);
