@@ -16,9 +16,13 @@
 // Renormalised gates are a softmax over the selected experts alone:
 //   w_j = p_j / sum_S p,   dlogit_{idx_j} += w_j (dw_j - sum_S w dw).
 //
-// Both kernels are bound by reading the logits (and writing their gradient):
-// one pass, each row held in registers by L lanes of 16 columns (32 past 512
-// experts), the softmax's maximum and sum by shuffles.
+// One pass over the logits, each row held in registers by L lanes of 16 columns
+// (32 past 512 experts), the softmax's maximum and sum by shuffles, the next row
+// in flight.  The bytes alone would take 2.8 us (loss, 65536 tokens of 128
+// experts, fp16) and 5.5 (gradient, bf16); issue slots bound both: the loss's
+// first pass takes about 10 us and its second 8 (a chain of dependent loads and
+// the last block's sums), the gradient 17.  A batch of 128 tokens takes one
+// launch of 7 us, the gradient of 4096 tokens of 256 experts 6.
 #include <type_traits>
 
 #include "common.cuh"

@@ -130,8 +130,8 @@ __global__ void __launch_bounds__(256) grad_reduce_kernel(const GradReduceArgs p
 // are spread over the adapters is on the device: some are taken to have twice
 // their even share, the longest CTA to run on for half its time.
 // A chunk's sum runs in the tensor cores' accumulator, which cuts off what it
-// cannot hold: past 2048 rows that would stand out beside a matrix product's in
-// fp32 (1.9e-6 of dB at 4096 rows, 0.8e-6 at 1500).
+// cannot hold: past 1024 rows that would stand out beside a matrix product's in
+// fp32 (1.9e-6 of dB with chunks of 2048 rows, 1.0e-6 with 1024; 0.5e-6 there).
 constexpr int kMaxChunk = 1024;
 struct Split {
   int chunk, cols;
@@ -235,7 +235,7 @@ int launch_lora_backward(const LoraBackwardArgs& q, cudaStream_t s) {
     ExpandArgs e{};
     e.h = image, e.M = static_cast<const __nv_bfloat16*>(q.A), e.offsets = q.offsets, e.order = q.order;
     e.n = q.n, e.rows = q.rows, e.N = q.d, e.R = q.R, e.base = q.dx_base, e.out = q.dx;
-    e.status = reinterpret_cast<int*>(ws);
+    e.status = reinterpret_cast<int*>(ws), e.apart = q.dA != nullptr;
     st = launch_lora_expand(e, true, q.dx_dtype, s);
     if (st != MOE_OK) return st;
   }

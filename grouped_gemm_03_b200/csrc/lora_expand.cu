@@ -5,11 +5,13 @@
 // out cross HBM once, so the kernel is a copy with a small product in its
 // middle.  A CTA takes up to 128 rows of one adapter and a slice of the
 // columns, 64 at a time: warps 0-3 bring the base tile and the adapter's
-// columns (TMA, the rows by gather4, into a ring of stages), one thread of warp 12 issues the
-// 128 x 64 MMAs into one of two accumulators, warps 4-7 add the accumulator to
-// the base tile in shared memory, where a thread holds a row, and write it out
-// from there, where 8 neighbouring lanes hold one: full 128-byte lines both
-// ways although the rows lie scattered.
+// columns (TMA, the rows by gather4, into a ring of stages), one thread of warp
+// 12 issues the 128 x 64 MMAs into one of two accumulators, warps 4-11 (two to a
+// quarter of the rows, half of the columns each) add the accumulator to the base
+// tile in shared memory, where a thread holds a row, and write it out from there,
+// where neighbouring lanes hold one: full sectors both ways although the rows lie
+// scattered.  Measured: 8192 rows of 4096 columns at rank 32, 29 us (4.6 TB/s
+// with its start; 5.8 while it streams).
 //
 // h comes split and laid out (lora_tc.cuh), scale and all, by one bulk copy: as
 // two bf16 terms (2^-17 of it left out) for a bf16 result and as three (all of
@@ -82,7 +84,7 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
   // start while it runs.
   int a, start, end;
   const bool found = find_tile(p.offsets, p.n, p.rows, kRows, blockIdx.x, a, start, end);
-  if (!found || a == p.n) {
+  if (!found || (a == p.n && !p.apart)) {
     pdl_wait();
     pdl_launch_dependents();
     if (!found) return;
@@ -100,8 +102,7 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
     if (p.h_out && blockIdx.y == 0)
       for (int i = tid; i < kRows * R; i += kExpandThreads)
         if (s_row[i / R] >= 0) p.h_out[static_cast<size_t>(s_row[i / R]) * R + i % R] = 0.f;
-    if (base == out) return;
-    const int w8 = (col1 - col0) / 8;
+    const int w8 = base == out ? 0 : (col1 - col0) / 8;
     for (int i = tid; i < kRows * w8; i += kExpandThreads) {
       const int r = s_row[i / w8];
       if (r < 0) continue;
@@ -110,16 +111,20 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
       if (base) load8(base + o, v);
       store8(out + o, v);
     }
+    if (p.apart) {
+      pdl_wait();
+      pdl_launch_dependents();
+    }
     return;
   }
   const int blocks = (col1 - col0 + kBC - 1) / kBC;
 
   __syncthreads();
   uint32_t tmem = 0;
-  if (warp >= kLoaders / 32) {   // TMEM only then: as in the streaming pass
-    pdl_wait();
+  if (warp >= kLoaders / 32) {   // TMEM only then: as in the streaming pass, which has its own before this one starts
+    if (!p.apart) pdl_wait();
     if (warp == kMmaWarp) {
-      pdl_launch_dependents();
+      if (!p.apart) pdl_launch_dependents();
       ptx::tmem_alloc(&s_tmem, 2 * kBC);
       ptx::tmem_relinquish();
     }
@@ -146,7 +151,7 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
     int t = 0;
     auto load_h = [&]() {
       if (warp) return;
-      pdl_wait();
+      if (!p.apart) pdl_wait();
       if (lane) return;
       ptx::mbar_arrive_expect_tx(&h_full, C::H);
       bulk_load(s_h, p.h + static_cast<size_t>(blockIdx.x) * RankTile<RP>::IMAGE, C::H, &h_full);
@@ -271,6 +276,10 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
   if (warp == kMmaWarp) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 2 * kBC);
+  }
+  if (p.apart) {   // what follows this launch follows the one beside it, too
+    pdl_wait();
+    pdl_launch_dependents();
   }
 }
 

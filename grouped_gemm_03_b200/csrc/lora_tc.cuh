@@ -163,6 +163,8 @@ struct ExpandArgs {
   const void* base;
   void* out;
   float* h_out;             // [rows, R] by row or nullptr: 0 for the rows without an adapter
+  bool apart;               // h is older than the launch before this one, and nothing here and there depends on the
+                            // other: this one runs beside it and waits for it at the end
   int* status;
 };
 int launch_lora_expand(ExpandArgs p, bool kn, int out_dtype, cudaStream_t s);
