@@ -604,7 +604,7 @@ struct RouterGradArgs {
 // selected experts' entries are then written over it by the lanes that hold
 // the slots (lane l slots l and l + L), which read their own logit again: a
 // search of the row's registers for k columns would cost more than the softmax.
-template <typename T, typename OT, int V, bool kRenorm>
+template <typename T, typename OT, int V, bool kRenorm, bool kTwo>
 __global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 1) router_backward_kernel(const RouterGradArgs a) {
   pdl_wait();
   pdl_launch_dependents();
@@ -624,18 +624,23 @@ __global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 1) router_backward_
   for (int i = 0; i < V; ++i) bal[i] = 0.f;
   const float d_loss = a.counts && a.d_loss ? __ldg(a.d_loss) : 1.f;
 
-  const bool two = k > L;   // slots to a lane
+  constexpr int U = kTwo ? 2 : 1;   // slots to a lane
   Row<T, V> next;
-  int next_e[2] = {-1, -1};
-  float next_g[2] = {0.f, 0.f};
+  int next_e[U];
+  float next_g[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) next_e[u] = -1, next_g[u] = 0.f;
+  bool next_kept = false;
+  int seq_end = !a.counts || s >= a.S ? 0 : a.off ? a.off[s + 1] : a.T;
+  const unsigned group_lanes = (L == 32 ? 0xffffffffu : (1u << L) - 1) << (lane & ~(L - 1));
   auto prefetch = [&](int t) {
     const bool live = t < t1;
     const size_t tr = live ? t : t0;
     next.load(logits + tr * E, E, L, l, a.vec);   // past the end an earlier row again, not written
+    next_kept = !a.mask || a.mask[tr];
     if (gates) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (u && !two) break;
+      for (int u = 0; u < U; ++u) {
         const bool in = live && l + u * L < k;
         next_e[u] = in ? __ldg(a.idx + tr * k + l + u * L) : -1;
         next_g[u] = in ? __ldg(a.d_w + tr * k + l + u * L) : 0.f;
@@ -649,24 +654,14 @@ __global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 1) router_backward_
     const int tr = live ? t : t0;
     const T* row = logits + static_cast<size_t>(tr) * E;
     Row<T, V> now = next;
-    int e[2] = {-1, -1};
-    float g[2] = {0.f, 0.f}, x[2] = {-INFINITY, -INFINITY};
-    if (gates) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (u && !two) break;
-        e[u] = next_e[u] >= 0 && next_e[u] < E ? next_e[u] : -1;
-        g[u] = e[u] >= 0 ? next_g[u] : 0.f;
-        if (e[u] >= 0) x[u] = to_f32(row[e[u]]);
-      }
-    }
-    // a slot without an expert whose gradient is not 0 still makes its row one to work on
-    const bool some = next_g[0] != 0.f || next_g[1] != 0.f;
-    if (b + groups < t1) prefetch(t + groups);
     bool in = false;
     if (a.counts) {
-      while (a.off && s < a.S && a.off[s + 1] <= tr) ++s;
-      in = s < a.S && (!a.mask || a.mask[tr]);
+      if (live)
+        while (s < a.S && seq_end <= tr) {
+          ++s;
+          seq_end = s < a.S ? a.off[s + 1] : 0;   // without offsets there is one sequence, which no token passes
+        }
+      in = live && s < a.S && next_kept;
       if (in && held != s) {
         held = s;
         c_s = __ldg(a.coef + s) * d_loss;
@@ -678,8 +673,20 @@ __global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 1) router_backward_
         }
       }
     }
+    int e[U];
+    float g[U], x[U], be[U];
+    bool some = false;   // a slot without an expert whose gradient is not 0 counts, too
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      e[u] = next_e[u] >= 0 && next_e[u] < E ? next_e[u] : -1;
+      g[u] = e[u] >= 0 ? next_g[u] : 0.f;
+      some |= next_g[u] != 0.f;
+      x[u] = e[u] >= 0 ? to_f32(row[e[u]]) : -INFINITY;
+      be[u] = e[u] >= 0 && in ? c_s * static_cast<float>(__ldg(a.counts + static_cast<size_t>(s) * E + e[u])) : 0.f;
+    }
+    if (b + groups < t1) prefetch(t + groups);
     // something to differentiate: else the row's gradient is 0 whatever its logits hold
-    const bool any = group_max(some ? 1.f : 0.f, L) != 0.f || in;
+    const bool any = (__ballot_sync(0xffffffffu, some) & group_lanes) != 0 || in;
     if (!any) now.clear();
     float p[V], m, inv;
     softmax_row(now, p, L, m, inv);
@@ -691,11 +698,10 @@ __global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 1) router_backward_
       for (int i = 0; i < V; ++i) dots[i & 1] = fmaf(p[i], bal[i], dots[i & 1]);
     }
     float dot = dots[0] + dots[1];
-    float ps[2] = {0.f, 0.f}, z = 0.f, wg = 0.f;
+    float ps[U], z = 0.f, wg = 0.f;
     if (gates) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (u && !two) break;
+      for (int u = 0; u < U; ++u) {
         ps[u] = e[u] >= 0 && any ? exp_from(x[u], m) * inv : 0.f;
         const float pg = e[u] >= 0 ? ps[u] * g[u] : 0.f;
         if (kRenorm)
@@ -706,15 +712,16 @@ __global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 1) router_backward_
     }
     dot = group_sum(dot, L);
     // the gradients of every slot that chose the same expert (one, as the router gives them)
-    float gs[2] = {0.f, 0.f}, ns[2] = {0.f, 0.f};
+    float gs[U], ns[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) gs[u] = ns[u] = 0.f;
     if (gates) {
       for (int j = 0; j < k; ++j) {
         const int from = (lane & ~(L - 1)) | (j & (L - 1));
-        const int ej = __shfl_sync(0xffffffffu, j < L ? e[0] : e[1], from);
-        const float gj = __shfl_sync(0xffffffffu, j < L ? g[0] : g[1], from);
+        const int ej = __shfl_sync(0xffffffffu, j < L ? e[0] : e[U - 1], from);
+        const float gj = __shfl_sync(0xffffffffu, j < L ? g[0] : g[U - 1], from);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (u && !two) break;
+        for (int u = 0; u < U; ++u) {
           gs[u] += ej == e[u] ? gj : 0.f;
           if (kRenorm) ns[u] += ej == e[u] ? 1.f : 0.f;
         }
@@ -750,15 +757,13 @@ __global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 1) router_backward_
     if (gates) {
       __syncwarp();   // the selected entries come after the row's
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (u && !two) break;
+      for (int u = 0; u < U; ++u) {
         if (!live || !any || e[u] < 0) continue;
-        const float be = in ? c_s * static_cast<float>(__ldg(a.counts + static_cast<size_t>(s) * E + e[u])) : 0.f;
         float v;
         if (kRenorm)
-          v = fmaf(ps[u] * inv_z, gs[u] - ns[u] * wg, ps[u] * (be - dot));
+          v = fmaf(ps[u] * inv_z, gs[u] - ns[u] * wg, ps[u] * (be[u] - dot));
         else
-          v = ps[u] * (be + gs[u] - dot);
+          v = ps[u] * (be[u] + gs[u] - dot);
         o[e[u]] = from_f32(v, OT());
       }
     }
@@ -791,14 +796,16 @@ int launch_partial(const BalanceArgs& a, int V, int cols, int w, cudaStream_t s)
   return launch_pdl(__func__, balance_partial_kernel<T, 32>, grid, block, smem, s, a);
 }
 
+template <typename T, typename OT, int V, bool kTwo>
+int launch_grad_rows(const RouterGradArgs& a, int grid, cudaStream_t s) {
+  const dim3 g(grid), b(kBalThreads);
+  return a.renorm ? launch_pdl("router_backward_kernel", router_backward_kernel<T, OT, V, true, kTwo>, g, b, 0, s, a)
+                  : launch_pdl("router_backward_kernel", router_backward_kernel<T, OT, V, false, kTwo>, g, b, 0, s, a);
+}
 template <typename T, typename OT>
 int launch_grad(const RouterGradArgs& a, int V, int grid, cudaStream_t s) {
-  const dim3 g(grid), b(kBalThreads);
-  if (V == 16)
-    return a.renorm ? launch_pdl(__func__, router_backward_kernel<T, OT, 16, true>, g, b, 0, s, a)
-                    : launch_pdl(__func__, router_backward_kernel<T, OT, 16, false>, g, b, 0, s, a);
-  return a.renorm ? launch_pdl(__func__, router_backward_kernel<T, OT, 32, true>, g, b, 0, s, a)
-                  : launch_pdl(__func__, router_backward_kernel<T, OT, 32, false>, g, b, 0, s, a);
+  if (V == 32) return launch_grad_rows<T, OT, 32, false>(a, grid, s);   // a whole warp to a row
+  return a.k > a.L ? launch_grad_rows<T, OT, 16, true>(a, grid, s) : launch_grad_rows<T, OT, 16, false>(a, grid, s);
 }
 
 template <typename T>
