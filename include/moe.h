@@ -326,7 +326,7 @@ int moe_combine_backward(const void* dout, int dout_dtype, const void* Y, const 
  *               = mean_s alpha * E * sum_e (counts / (k N_s)) * prob
  *   logits      [T, E] dtype MOE_F32 | MOE_F16 | MOE_BF16 (moe_router_topk's logits_out, say).
  *               A logit of -inf has probability 0; a token whose logits are all -inf adds
- *               none to prob.  What a token that does not count holds is not read.
+ *               none to prob.  What a token that does not count holds does not matter.
  *   topk_idx    [T, k] int32; -1 is a slot without an expert (not counted)
  *   seq_offsets [S+1] int32 DEVICE array, seq_offsets[0] = 0, non-decreasing,
  *               <= T; tokens from seq_offsets[S] on belong to no sequence.

@@ -225,3 +225,39 @@ def test_captured_on_a_side_stream_and_replayed():
             assert torch.equal(a, b)
         assert torch.equal(d, gg.router_backward(l, i, g, counts=eager[1], coef=eager[3], seq_offsets=o, mask=m))
         _check_loss(eager, tuning.balance_loss(fresh, idx2, 0.1, offsets, mask))
+
+
+# many short sequences, more of them than a block has threads, slots past eight, chunks past a block's threads
+@pytest.mark.parametrize("T,E,k,S,dtype", [(3000, 96, 9, 400, torch.bfloat16), (600, 1000, 32, 590, torch.float32),
+                                           (120000, 8, 2, 300, torch.float16), (130001, 24, 1, None, torch.bfloat16),
+                                           (2000, 7, 3, 2, torch.float32)])
+def test_balance_loss_of_large_batches(T, E, k, S, dtype):
+    logits, idx, offsets, mask = _inputs(T, E, k, S, dtype, True, seed=12)
+    ws = torch.empty(gg.lib().moe_balance_loss_workspace_size(T, E, S or 1), dtype=torch.uint8, device=DEV)
+    args = _dev(logits), _dev(idx), 0.5, _dev(offsets, torch.int32), _dev(mask)
+    ws.fill_(0xff)
+    got = gg.balance_loss(*args, ws=ws)
+    assert gg.read_device_status(ws) == 0
+    _check_loss(got, tuning.balance_loss(logits, idx, 0.5, offsets, mask))
+    for a, b in zip(got, gg.balance_loss(*args)):   # bit for bit, whatever the workspace held
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_rows_of_the_types_lowest_value(dtype):
+    T, E, k = 40, 24, 3
+    logits = torch.randn(T, E, generator=torch.Generator().manual_seed(2)).to(dtype)
+    low = torch.finfo(dtype).min
+    logits[3] = low                       # all equal: an even row
+    logits[4, 1:] = low
+    logits[5] = float("-inf")
+    logits[6, :20] = float("-inf")
+    logits[6, 20:] = low                  # even over the last four
+    logits[7] = torch.finfo(dtype).max    # even, too
+    idx = torch.tensor([[0, 21, 22]] * T, dtype=torch.int32)
+    g = torch.randn(T, k)
+    got = gg.balance_loss(_dev(logits), _dev(idx), 1.0)
+    _check_loss(got, tuning.balance_loss(logits, idx, 1.0))
+    d = gg.router_backward(_dev(logits), _dev(idx), _dev(g), counts=got[1], coef=got[3])
+    want = tuning.router_backward(logits, idx, g, False, (got[1].cpu().numpy(), got[3].cpu().numpy(), 1.0, None, None))
+    np.testing.assert_allclose(d.cpu().numpy(), want, rtol=0, atol=20 * EPS * (1 + np.abs(want).max()))
