@@ -541,10 +541,10 @@ __global__ void __launch_bounds__(kBalThreads) balance_finish_kernel(const Balan
     }
   }
   __syncthreads();
-  if (tid == 0) {
-    __threadfence();   // the block's results, which the barrier has brought here, before its arrival
-    s_last = atomicAdd(a.done, 1) == static_cast<int>(gridDim.x) - 1;
-    __threadfence();
+  if (tid == 0) {   // the block's results, which the barrier has brought here, before its arrival; the others' after it
+    int before;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(a.done) : "memory");
+    s_last = before == static_cast<int>(gridDim.x) - 1;
   }
   __syncthreads();
   if (!s_last) return;
@@ -553,7 +553,9 @@ __global__ void __launch_bounds__(kBalThreads) balance_finish_kernel(const Balan
 #pragma unroll 4
   for (long long i = tid; i < tasks; i += kBalThreads) sum += __ldcg(a.share + i);
   for (int i = tid; i < a.chunks; i += kBalThreads) err |= a.part_err[i];
-  for (int s = tid; s < a.S; s += kBalThreads) live += __ldcg(a.tokens + s) > 0;
+  const int first = tid < a.S ? __ldcg(a.tokens + tid) : 0;
+  live = first > 0;
+  for (int s = tid + kBalThreads; s < a.S; s += kBalThreads) live += __ldcg(a.tokens + s) > 0;
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   live = __reduce_add_sync(0xffffffffu, live);
@@ -564,7 +566,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_finish_kernel(const Balan
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) sum += s_sum[w], live += s_n[w], err |= s_c[w][0];
   for (int s = tid; s < a.S; s += kBalThreads) {
-    const float nf = static_cast<float>(__ldcg(a.tokens + s));
+    const float nf = static_cast<float>(s == tid ? first : __ldcg(a.tokens + s));
     a.coef[s] = nf > 0.f ? __fdiv_rn(a.alpha * E, a.k * nf * nf * static_cast<float>(live)) : 0.f;
   }
   if (tid == 0) {
