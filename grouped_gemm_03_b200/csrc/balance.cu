@@ -32,7 +32,6 @@ namespace {
 
 constexpr int kBalThreads = 256;
 constexpr int kBalMinChunk = 32;     // tokens of one block, at least
-constexpr int kBalMaxChunks = 444;   // blocks of the first pass: three on each of 148 SMs, all at once
 constexpr int kBalSmall = 512;       // tokens up to which one cluster does both passes
 constexpr int kFinCluster = 8;       // CTAs of a small batch's second pass, each a slice of the experts
 
@@ -469,7 +468,7 @@ __device__ void balance_finish(const BalanceArgs& a, int cols, int w) {
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 1) balance_partial_kernel(const BalanceArgs a) {
+__global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 2) balance_partial_kernel(const BalanceArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   extern __shared__ float s_mem[];
@@ -607,7 +606,7 @@ struct RouterGradArgs {
 // the slots (lane l slots l and l + L), which read their own logit again: a
 // search of the row's registers for k columns would cost more than the softmax.
 template <typename T, typename OT, int V, bool kRenorm, bool kTwo>
-__global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 1) router_backward_kernel(const RouterGradArgs a) {
+__global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 2) router_backward_kernel(const RouterGradArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   const int E = a.E, L = a.L, k = a.k;
@@ -779,9 +778,13 @@ int lanes_for(int E, int V) {  // lanes of a row: a power of two, V columns each
 }
 int values_for(int E) { return E <= 512 ? 16 : 32; }
 
-int balance_chunk(int T) {
+// Blocks that run at once: three to an SM of 148, two where a lane holds 32 columns (with one, 8192 tokens of 1024
+// experts in bf16 took the gradient 29.4 us in three waves, 18.8 in one of two to an SM).
+int blocks_at_once(int E) { return 148 * (values_for(E) == 16 ? 3 : 2); }
+
+int balance_chunk(int T, int E) {
   if (T <= kBalSmall) return T > 0 ? (T + kFinCluster - 1) / kFinCluster : 1;
-  const int c = (T + kBalMaxChunks - 1) / kBalMaxChunks;
+  const int c = (T + blocks_at_once(E) - 1) / blocks_at_once(E);
   return c < kBalMinChunk ? kBalMinChunk : c;
 }
 
@@ -820,7 +823,7 @@ int launch_grad_to(const RouterGradArgs& a, int out_dtype, int V, int grid, cuda
 }  // namespace
 
 size_t balance_workspace_bytes(int T, int E, int S) {
-  const size_t chunks = T > 0 ? (T + balance_chunk(T) - 1) / balance_chunk(T) : 0;
+  const size_t chunks = T > 0 ? (T + balance_chunk(T, E) - 1) / balance_chunk(T, E) : 0;
   const size_t slots = chunks + S;
   const size_t tasks = T > kBalSmall ? static_cast<size_t>(S) * ((E + kFinCols - 1) / kFinCols) + S : 0;
   return 256 + align_up(slots * E * 4, 256) * 2 + align_up(slots * 4, 256) + align_up(chunks * 4 + 4, 256) +
@@ -833,7 +836,7 @@ int launch_balance_loss(const void* logits, int dtype, const int32_t* idx, int T
   BalanceArgs a{};
   const int V = values_for(E);
   a.logits = logits, a.idx = idx, a.T = T, a.E = E, a.k = k, a.off = off, a.S = S, a.mask = mask, a.alpha = alpha;
-  a.chunk = balance_chunk(T);
+  a.chunk = balance_chunk(T, E);
   a.chunks = T > 0 ? (T + a.chunk - 1) / a.chunk : 0;
   a.L = lanes_for(E, V);
   a.vec = E % (dtype == MOE_F32 ? 4 : 8) != 0 ? 0 : E == a.L * V ? 2 : 1;
@@ -877,7 +880,7 @@ int launch_router_backward(const void* logits, int dtype, const int32_t* idx, co
   while (a.L * 2 < k) a.L *= 2;   // two slots to a lane
   a.vec = E % (dtype == MOE_F32 ? 4 : 8) != 0 ? 0 : E == a.L * V ? 2 : 1;   // not 0: rows of every output type are stored whole too
   const int groups = kBalThreads / a.L;
-  const int blocks = num_sms() * 3;   // one wave
+  const int blocks = blocks_at_once(E);
   a.chunk = (T + blocks - 1) / blocks;
   a.chunk = (a.chunk + groups - 1) / groups * groups;
   const int grid = (T + a.chunk - 1) / a.chunk;
