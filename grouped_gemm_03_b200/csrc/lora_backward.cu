@@ -6,7 +6,8 @@
 // over x gives dA, and the forward's second product, with A in the place of B,
 // gives dx.  Each wide operand is read once; what several CTAs add to is
 // written as partial sums and added here in a fixed order, so results do not
-// vary from run to run.
+// vary from run to run.  Adapters of few rows take one launch instead
+// (lora_few.cu).
 #include "common.cuh"
 #include "lora.cuh"
 #include "lora_tc.cuh"
@@ -159,7 +160,17 @@ Split split_for(int rows, int n, int W, int R, bool proj) {
   return best;
 }
 
+// Whether one launch on tiles of few rows does it all (lora_few.cu): with up to
+// four rows to an adapter, and above rank 32 from eight adapters on.  Measured,
+// that launch against the streaming passes, columns 4096 and 4096:
+//   rank 16: 1 row of 1 adapter 9.1 / 13.9 us, 4 of 1 9.3 / 13.9, 8 of 1 15.5 / 14.4, 30 of 30 15.5 / 34.8,
+//            500 of 128 94 / 114, 64 of 8 21.4 / 21.3, 500 of 64 64.8 / 64.6
+//   rank 64: 2 of 1 22.3 / 16.2, 8 of 8 22.7 / 30.9, 32 of 32 41 / 91, 64 of 8 54 / 28, 500 of 64 172 / 159
+// and of 2048 columns at rank 64 100 of 100 61 / 145, at rank 128 131 / 188.
+bool few_rows(int rows, int n, int R) { return rows <= 4ll * n && (R <= 32 || n >= 8); }
+
 struct BackwardLayout {
+  bool few;
   Split dc, x;
   size_t dh_part, image, pA, pB, total;
 };
@@ -171,6 +182,14 @@ BackwardLayout backward_layout(int rows, int n, int d, int N, int R) {
     off = align_up(off + bytes, 256);
     return o;
   };
+  L.few = few_rows(rows, n, R);
+  if (L.few) {
+    L.dc = L.x = Split{kRowsFew, 0};
+    L.pA = take(part_slot(rows, kRowsFew) * R * d * 4);
+    L.pB = take(part_slot(rows, kRowsFew) * R * N * 4);
+    L.total = off;
+    return L;
+  }
   L.dc = split_for(rows, n, N, R, true);
   L.x = split_for(rows, n, d, R, false);
   const size_t slices = (N + L.dc.cols - 1) / L.dc.cols;
@@ -201,43 +220,48 @@ int launch_lora_backward(const LoraBackwardArgs& q, cudaStream_t s) {
     if (q.dB) MOE_CUDA_CHECK(cudaMemsetAsync(q.dB, 0, q.n * sizeB * bytes, s));
     return MOE_OK;
   }
-  const bool need_dh = q.dx || q.dA;
-  TermsArgs t{};
-  t.scale = q.scale, t.offsets = q.offsets, t.order = q.order, t.n = q.n, t.rows = q.rows, t.R = q.R, t.image = image;
   int st = MOE_OK;
-  if (q.dB) {
-    t.h = q.h;
-    st = launch_terms<false>(t, s);
+  if (L.few) {
+    st = launch_lora_few(q, reinterpret_cast<float*>(ws + L.pA), reinterpret_cast<float*>(ws + L.pB), s);
     if (st != MOE_OK) return st;
-  }
-  StreamArgs p{};
-  p.X = static_cast<const __nv_bfloat16*>(q.dC), p.M = static_cast<const __nv_bfloat16*>(q.B), p.V = image;
-  p.scale = q.scale, p.offsets = q.offsets, p.order = q.order, p.n = q.n, p.rows = q.rows, p.W = q.N, p.R = q.R;
-  p.chunk = L.dc.chunk, p.cols = L.dc.cols, p.early = q.dB != nullptr;
-  p.proj = need_dh ? dh_part : nullptr;
-  p.part = reinterpret_cast<float*>(ws + L.pB), p.grad = q.dB, p.grad_f32 = q.grad_dtype == MOE_F32;
-  p.status = reinterpret_cast<int*>(ws), p.first = true;
-  st = launch_lora_stream(p, kStreamBoth, s);
-  if (st != MOE_OK) return st;
-  if (need_dh) {
-    t.h = dh_part, t.slices = (q.N + L.dc.cols - 1) / L.dc.cols;
-    st = launch_terms<true>(t, s);
+  } else {
+    const bool need_dh = q.dx || q.dA;
+    TermsArgs t{};
+    t.scale = q.scale, t.offsets = q.offsets, t.order = q.order, t.n = q.n, t.rows = q.rows, t.R = q.R, t.image = image;
+    if (q.dB) {
+      t.h = q.h;
+      st = launch_terms<false>(t, s);
+      if (st != MOE_OK) return st;
+    }
+    StreamArgs p{};
+    p.X = static_cast<const __nv_bfloat16*>(q.dC), p.M = static_cast<const __nv_bfloat16*>(q.B), p.V = image;
+    p.scale = q.scale, p.offsets = q.offsets, p.order = q.order, p.n = q.n, p.rows = q.rows, p.W = q.N, p.R = q.R;
+    p.chunk = L.dc.chunk, p.cols = L.dc.cols, p.early = q.dB != nullptr;
+    p.proj = need_dh ? dh_part : nullptr;
+    p.part = reinterpret_cast<float*>(ws + L.pB), p.grad = q.dB, p.grad_f32 = q.grad_dtype == MOE_F32;
+    p.status = reinterpret_cast<int*>(ws), p.first = true;
+    st = launch_lora_stream(p, kStreamBoth, s);
     if (st != MOE_OK) return st;
-  }
-  if (q.dA) {
-    p.X = static_cast<const __nv_bfloat16*>(q.x), p.M = nullptr, p.W = q.d;
-    p.chunk = L.x.chunk, p.cols = L.x.cols, p.early = true, p.first = false, p.proj = nullptr;
-    p.part = reinterpret_cast<float*>(ws + L.pA), p.grad = q.dA;
-    st = launch_lora_stream(p, kStreamGrad, s);
-    if (st != MOE_OK) return st;
-  }
-  if (q.dx) {
-    ExpandArgs e{};
-    e.h = image, e.M = static_cast<const __nv_bfloat16*>(q.A), e.offsets = q.offsets, e.order = q.order;
-    e.n = q.n, e.rows = q.rows, e.N = q.d, e.R = q.R, e.base = q.dx_base, e.out = q.dx;
-    e.status = reinterpret_cast<int*>(ws), e.apart = q.dA != nullptr;
-    st = launch_lora_expand(e, true, q.dx_dtype, s);
-    if (st != MOE_OK) return st;
+    if (need_dh) {
+      t.h = dh_part, t.slices = (q.N + L.dc.cols - 1) / L.dc.cols;
+      st = launch_terms<true>(t, s);
+      if (st != MOE_OK) return st;
+    }
+    if (q.dA) {
+      p.X = static_cast<const __nv_bfloat16*>(q.x), p.M = nullptr, p.W = q.d;
+      p.chunk = L.x.chunk, p.cols = L.x.cols, p.early = true, p.first = false, p.proj = nullptr;
+      p.part = reinterpret_cast<float*>(ws + L.pA), p.grad = q.dA;
+      st = launch_lora_stream(p, kStreamGrad, s);
+      if (st != MOE_OK) return st;
+    }
+    if (q.dx) {
+      ExpandArgs e{};
+      e.h = image, e.M = static_cast<const __nv_bfloat16*>(q.A), e.offsets = q.offsets, e.order = q.order;
+      e.n = q.n, e.rows = q.rows, e.N = q.d, e.R = q.R, e.base = q.dx_base, e.out = q.dx;
+      e.status = reinterpret_cast<int*>(ws), e.apart = q.dA != nullptr;
+      st = launch_lora_expand(e, true, q.dx_dtype, s);
+      if (st != MOE_OK) return st;
+    }
   }
   // an adapter of several chunks has to have more rows than one holds
   const bool manyA = q.dA && q.rows > L.x.chunk, manyB = q.dB && q.rows > L.dc.chunk;

@@ -152,6 +152,11 @@ enum StreamKind { kStreamProject, kStreamBoth, kStreamGrad };
 int launch_lora_stream(const StreamArgs& p, StreamKind kind, cudaStream_t s);
 int lora_stream_max_cols(int R, bool proj);  // columns of a CTA that forms G, at most
 
+// The gradients where an adapter has few rows, in one launch on tiles of kRowsFew rows (lora_few.cu); partial
+// sums of adapters of more, by part_slot(offset, kRowsFew)
+constexpr int kRowsFew = 16;
+int launch_lora_few(const LoraBackwardArgs& q, float* part_A, float* part_B, cudaStream_t s);
+
 // out[r] = base[r] + h[r] W_a (lora_expand.cu)
 struct ExpandArgs {
   const uint8_t* h;         // images of h's terms, scaled, by tile slot

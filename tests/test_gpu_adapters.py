@@ -332,6 +332,31 @@ def test_two_launches(rows, n, d, N, R, only, dtype):
     assert torch.equal(odd[~mine], plain[~mine]) and not torch.isfinite(odd[mine]).any()
 
 
+# gradients of few rows to an adapter, in one launch: alone, ragged (some of more tiles than one), every rank
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,n,d,N,R,only", [(1, 1, 8, 8, 8, None), (4, 1, 4096, 136, 32, None), (3, 2, 72, 1032, 24, [1]),
+                                               (61, 48, 264, 520, 16, None), (100, 100, 520, 264, 64, None),
+                                               (160, 40, 136, 2056, 104, [0, 0, 0, 5, 39, -1]), (32, 8, 648, 72, 40, [7]),
+                                               (200, 1024, 64, 64, 8, None), (33, 9, 2048, 2816, 128, None)])
+def test_backward_of_few_rows(rows, n, d, N, R, only, dtype):
+    s = _inputs(rows, n, d, N, R, seed=rows + R, only=only)
+    h = torch.from_numpy(np.random.default_rng(6).normal(size=(rows, R)).astype(np.float32))
+    dC, x, A, B, scale = _gpu(s, "dC", "x", "A", "B", "scale")
+    base = s["dx_base"].to(dtype)
+    off, order = _plan(s, n)
+    ws = torch.empty(gg.lib().moe_lora_backward_workspace_size(rows, n, d, N, R), dtype=torch.uint8, device=DEV)
+    ws.fill_(0xff)
+    got = gg.lora_backward(dC, x, h.to(DEV), A, B, off, order, scale=scale, dx_base=base.to(DEV), grad_dtype=dtype, ws=ws)
+    assert gg.read_device_status(ws) == 0
+    _check_backward(s, got, h, s["scale"], base)
+    y = base.to(DEV)
+    assert torch.equal(gg.lora_backward(dC, x, h.to(DEV), A, B, off, order, scale=scale, dx_base=y, dx=y,
+                                        want_grads=False)[0], got[0])
+    dx = gg.lora_backward(dC, x, h.to(DEV), A, B, off, order, want_grads=False, dx_dtype=dtype)[0]
+    dA, dB = gg.lora_backward(dC, x, h.to(DEV), A, B, off, order, want_dx=False)[1:]
+    _check_backward(s, (dx, dA, dB), h, None, None)
+
+
 # adapters of several chunks of a gradient
 @pytest.mark.parametrize("rows,n,d,N,R,only", [(2600, 2, 512, 392, 16, [0]), (2600, 3, 264, 512, 32, [0, 0, 2]),
                                                (3100, 2, 1160, 648, 64, [1]), (2300, 2, 256, 384, 128, [0, 0, 1])])
@@ -364,7 +389,7 @@ def test_what_a_workspace_holds_does_not_show(rows, n, d, N, R):
         assert all(torch.equal(u, v) for u, v in zip(got[0], other))
 
 
-@pytest.mark.parametrize("rows", [30, 400])
+@pytest.mark.parametrize("rows", [8, 30, 400])
 def test_another_adapters_values_stay_its_own(rows):
     # weights, rows and gradients that are not finite reach nothing of another adapter, whichever lies beside it
     n, d, N, R = 3, 136, 72, 24
