@@ -366,13 +366,12 @@ int launch_lora_tiles(LoraArgs& p, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   const int st = allow_smem(done, kernel, L::SMEM);
   if (st != MOE_OK) return st;
-  // as many CTAs as are resident together, two to an SM up to rank 64 (a second wave took 11.3 us where one takes
-  // 6.8: 61 rows of 48 adapters, clusters of 8 against 4), each with at least 128 columns of the wider side
+  // as many CTAs as are resident together: a second wave took 11.3 us where one takes 6.8 (61 rows of 48 adapters,
+  // clusters of 8 against 4)
   const long long half_full = p.rows / MT + p.n / 2, one_each = p.n < p.rows ? p.n : p.rows;
-  const long long tiles = half_full > one_each ? half_full : one_each, room = (RP <= 64 ? 2ll : 1ll) * num_sms();
-  const int widest = p.d > p.N ? p.d : p.N;
-  int cs = 1;
-  while (cs < 8 && 2 * tiles * cs <= room && widest >= cs * 2 * 128) cs *= 2;
+  static std::atomic<int> known[9] = {};
+  const int cs = cluster_for(known, kernel, kLoraThreads, L::SMEM, half_full > one_each ? half_full : one_each,
+                             p.d > p.N ? p.d : p.N);
   p.kslice = ((p.d + cs - 1) / cs + 31) / 32 * 32;
   p.nslice = ((p.N + cs - 1) / cs + 31) / 32 * 32;
   return launch_cluster("lora_kernel", kernel, dim3(static_cast<unsigned>(tile_slots<MT>(p.rows, p.n) * cs)),

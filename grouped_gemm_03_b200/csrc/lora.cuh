@@ -92,6 +92,43 @@ int allow_smem(std::atomic<uint64_t>& done, K kernel, int bytes) {
   return MOE_OK;
 }
 
+// How many clusters of `cs` CTAs of `kernel` are resident together (0: the runtime does not say); `known` (one
+// per kernel and size) holds the answer.  A cluster lies within one group of SMs: with two CTAs to an SM 148 pairs
+// fit, but only 71 fours and 33 eights.
+template <typename K>
+int resident_clusters(std::atomic<int>& known, K kernel, int threads, size_t smem, int cs) {
+  int n = known.load();
+  if (n > 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cs);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cs;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();   // an estimate only: the launch itself reports what is wrong
+    n = 0;
+  }
+  known.store(n);
+  return n;
+}
+
+// The largest cluster, up to eight CTAs, with which `tiles` clusters are resident together and each CTA has at
+// least 128 of `widest` columns.  `tiles` is an average over how the rows may lie; a margin of a sixteenth saved a
+// second wave where they lay worse (1021 rows of 12 adapters, rank 64: 28 -> 22 us) and cost as much where they did
+// not (18 -> 21).
+template <typename K>
+int cluster_for(std::atomic<int> (&known)[9], K kernel, int threads, size_t smem, long long tiles, int widest) {
+  int cs = 1;
+  while (cs < 8 && widest >= (cs + 1) * 128 && tiles <= resident_clusters(known[cs + 1], kernel, threads, smem, cs + 1)) ++cs;
+  return cs;
+}
+
 // Launch `kernel` in clusters of `cs` CTAs, allowed to start while the kernel before it finishes.
 template <typename... Params, typename... Args>
 int launch_cluster(const char* where, void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, int cs,

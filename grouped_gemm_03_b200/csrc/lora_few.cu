@@ -311,12 +311,10 @@ int launch_few(const LoraBackwardArgs& q, FewParts w, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   const int st = allow_smem(done, kernel, F::SMEM);
   if (st != MOE_OK) return st;
-  // as many CTAs as are resident together, two to an SM up to rank 64, each with at least 128 columns of the wider side
   const long long half_full = q.rows / kRowsFew + q.n / 2, one_each = q.n < q.rows ? q.n : q.rows;
-  const long long tiles = half_full > one_each ? half_full : one_each;
-  const int widest = q.d > q.N ? q.d : q.N;
-  int cs = 1;
-  while (cs < 8 && 2 * tiles * cs <= (RP <= 64 ? 2ll : 1ll) * num_sms() && widest >= cs * 2 * 128) cs *= 2;
+  static std::atomic<int> known[9] = {};
+  const int cs = cluster_for(known, kernel, kFewThreads, F::SMEM, half_full > one_each ? half_full : one_each,
+                             q.d > q.N ? q.d : q.N);
   w.kslice = ((q.d + cs - 1) / cs + 63) / 64 * 64;
   w.nslice = ((q.N + cs - 1) / cs + 63) / 64 * 64;
   return launch_cluster("lora_few_kernel", kernel, dim3(static_cast<unsigned>(tile_slots<kRowsFew>(q.rows, q.n) * cs)),
