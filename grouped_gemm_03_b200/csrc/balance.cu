@@ -182,10 +182,10 @@ __device__ __forceinline__ float exp_from(float v, float m) {
   return fabsf(m) < kPlain ? exp2_of(fmaf(v, kLog2e, -m * kLog2e)) : exp2_of((v - m) * kLog2e);
 }
 
-// The numerators e^(v - m) of a row's softmax, with the row's maximum m and 1 / (their sum).  A logit of -inf has probability 0; a
-// row of nothing else (a row that is not live is one) has probability 0
-// throughout: inv = 0.  The maximum passes over a NaN, the sum does not, so a
-// NaN logit makes its row NaN.
+// The numerators e^(v - m) of a row's softmax, with the row's maximum m and
+// 1 / (their sum).  A logit of -inf has probability 0; a row of nothing else (a
+// row that is not live is one) has probability 0 throughout: inv = 0.  The
+// maximum passes over a NaN, the sum does not, so a NaN logit makes its row NaN.
 template <typename T, int V>
 __device__ __forceinline__ void softmax_row(const Row<T, V>& row, float (&v)[V], int L, float& m, float& inv) {
   m = group_max(row.largest(), L);
