@@ -174,10 +174,12 @@ __device__ __forceinline__ float exp2_of(float x) {
 }
 constexpr float kLog2e = 1.44269504f;
 // e^(v - m), m a row's maximum.  One multiply-add v log2 e - m log2 e serves a
-// row whose maximum is within kPlain: the rounding of m log2 e is common to the
-// row and falls out of its softmax.  Past it (a row of nothing but the type's
-// lowest value) the products would overflow, and v - m comes first.
-constexpr float kPlain = 1e30f;
+// row whose maximum is within kPlain: the rounding of m log2 e, at most 2^-4
+// there (half a step below 2^21), is common to the row and falls out of its
+// softmax.  Past it that rounding grows with m (440 at 1e10, more than an
+// exponent holds), and v - m comes first: exact next to m, and far from it the
+// numerator is 0 either way.
+constexpr float kPlain = 1048576.f;
 __device__ __forceinline__ float exp_from(float v, float m) {
   return fabsf(m) < kPlain ? exp2_of(fmaf(v, kLog2e, -m * kLog2e)) : exp2_of((v - m) * kLog2e);
 }

@@ -261,3 +261,41 @@ def test_rows_of_the_types_lowest_value(dtype):
     d = gg.router_backward(_dev(logits), _dev(idx), _dev(g), counts=got[1], coef=got[3])
     want = tuning.router_backward(logits, idx, g, False, (got[1].cpu().numpy(), got[3].cpu().numpy(), 1.0, None, None))
     np.testing.assert_allclose(d.cpu().numpy(), want, rtol=0, atol=20 * EPS * (1 + np.abs(want).max()))
+
+
+def _large_rows(T, E, dtype, seed):
+    """Finite rows whose maximum is far from 0, between the types' borders, among ordinary ones."""
+    l = torch.randn(T, E, generator=torch.Generator().manual_seed(seed))
+    at = 1
+    for m in (1e6, 2.0 ** 20 - 1, 2.0 ** 20 + 1, 3e7, 1e9, 1e10, 1e12, 1e15, 1e20, 1e29, 1e31):
+        for v in (m, -m):
+            l[at] = v                                     # all equal: an even row
+            l[at + 1] = v
+            l[at + 1, 1::2] = -1e35                       # even over half of them
+            l[at + 2, 1:], l[at + 2, 0] = v, 2 * abs(v)   # one takes all
+            l[at + 3] = v + torch.arange(E) % 7 * 0.5     # as far apart as the type holds there
+            at += 5                                       # an ordinary row between
+    return l.to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,E", [(120, 24), (700, 128), (120, 999), (600, 1024)])
+def test_large_finite_rows(T, E, dtype):
+    """The exponent's argument is (l - m) log2 e in fp32 there too, so the tolerances of ordinary rows hold."""
+    k = 3
+    logits = _large_rows(T, E, dtype, seed=E)
+    idx = np.argsort(-logits.float().numpy(), axis=1, kind="stable")[:, :k].astype(np.int32)
+    idx[::2, 2] = E - 1
+    offsets = np.array([0, T // 3, T])
+    got = gg.balance_loss(_dev(logits), _dev(idx), 1.0, _dev(offsets, torch.int32))
+    _check_loss(got, tuning.balance_loss(logits, idx, 1.0, offsets))
+    p = tuning.softmax_rows(logits)
+    g = np.random.default_rng(3).normal(size=(T, k)).astype(np.float32)
+    counts, coef = got[1].cpu().numpy(), got[3].cpu().numpy()
+    for renorm in (False, True):
+        d = gg.router_backward(_dev(logits), _dev(idx), _dev(g), renorm, counts=got[1], coef=got[3],
+                               seq_offsets=_dev(offsets, torch.int32))
+        want = tuning.router_backward(logits, idx, g, renorm, (counts, coef, 1.0, offsets, None))
+        sel = np.take_along_axis(p, idx, 1).sum(1, keepdims=True) if renorm else 1.0
+        G = np.abs(g).max(1, keepdims=True) / sel + coef.max() * counts.max()
+        _check_grad(d, want, p, G, renorm_extra=1.0 if renorm else 0.0)
