@@ -54,7 +54,7 @@ int64_t dim(const at::Tensor& t, const char* what, int dims, int i) {
 }
 
 int as_int(int64_t v, const char* what) {
-  if (v > INT32_MAX) fail(PyExc_ValueError, "%s: %lld is past 32 bits", what, static_cast<long long>(v));
+  if (v > INT32_MAX || v < INT32_MIN) fail(PyExc_ValueError, "%s: %lld is past 32 bits", what, static_cast<long long>(v));
   return static_cast<int>(v);
 }
 
@@ -248,10 +248,11 @@ PyObject* adapter_plan(PyObject* const* a) {
   const long n = PyLong_AsLong(a[1]);
   if (n == -1 && PyErr_Occurred()) throw Error();
   const at::Tensor* ws = tensor(a[2], "ws", true);
+  const int nn = as_int(n, "adapters");   // first: offsets is made for n, the kernels write nn + 1 entries
   const Call c(row);
   const int64_t rows = row.numel();
   const int* p_r = static_cast<int*>(c.at(&row, "row_adapter", kI32, {rows}));
-  const int nr = as_int(rows, "rows"), nn = as_int(n, "adapters");
+  const int nr = as_int(rows, "rows");
   at::Tensor keep;
   size_t bytes;
   void* p_ws = c.workspace(ws, moe_adapter_plan_workspace_size(nr, nn), keep, bytes);

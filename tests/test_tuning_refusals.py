@@ -127,3 +127,10 @@ def test_binding_refuses_what_is_no_tensor():
         gg.adapter_plan(None, 2)
     with pytest.raises(TypeError):
         gg.lora(1, 2, 3, 4, 5)
+
+
+@pytest.mark.parametrize("n", [(1 << 31), (1 << 32) + 5, -(1 << 32) + 5, -(1 << 31) - 1])
+def test_binding_refuses_adapters_past_32_bits(n):
+    # a number cut to 32 bits would pass for another one, and offsets is made for the one that was asked for
+    with pytest.raises(ValueError, match="adapters"):
+        gg.adapter_plan(torch.zeros(4, dtype=torch.int32), n)
