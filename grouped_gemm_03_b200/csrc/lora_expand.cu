@@ -156,7 +156,10 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
       ptx::mbar_arrive_expect_tx(&h_full, C::H);
       bulk_load(s_h, p.h + static_cast<size_t>(blockIdx.x) * RankTile<RP>::IMAGE, C::H, &h_full);
     };
-    for (; t < blocks; ++t) {
+    // A warp without rows of base to bring stays out of the loop: the stages would turn without it, and a barrier
+    // could turn twice between two of its looks.  Warp 0 brings the weights.
+    const int mine = warp == 0 || (base && warp * 8 < quads) ? blocks : 0;
+    for (; t < mine; ++t) {
       if (t == S) load_h();   // the ring is full
       if (t >= S && !ptx::mbar_wait_warp(&empty[t % S], (t / S - 1) & 1, abort_flag, kWaitLimitNs)) {
         give_up();

@@ -226,7 +226,10 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
     const uint8_t* image = p.V + static_cast<size_t>(first / kTile + a + (start - first) / kTile) * RT::IMAGE;
     bool ok = true;
     int t = 0;
-    for (int step = 0; step < steps && ok; ++step) {
+    // A warp with rows to bring is part of every stage's turn, so that none passes it unseen; one without stays out
+    // of the loop, where a barrier could turn twice between two of its looks.
+    const int my_steps = warp * Q < quads ? steps : 0;
+    for (int step = 0; step < my_steps && ok; ++step) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) row[u] = next[u] >= 0 && next[u] < p.rows ? next[u] : p.rows;
       if (step + 1 < steps) fetch_ids(step + 1);

@@ -420,3 +420,40 @@ def test_gradients_past_32_bit_offsets():
     off, order = gg.adapter_plan(row, 1)
     dx, dA, dB = gg.lora_backward(dC, x, torch.full((rows, R), 2.0, device=DEV), A, B, off, order, dx_dtype=torch.float32)
     assert (dx[-3:] == N * R).all() and not dx[:-3].any() and (dA == 3 * N).all() and (dB == 6).all()
+
+
+def _ragged(counts, d, N, R, seed):
+    """Rows of each adapter as counted, in a shuffled batch."""
+    r = np.random.default_rng(seed)
+    s = _inputs(sum(counts), len(counts), d, N, R, seed=seed)
+    s["row"] = r.permutation(np.repeat(np.arange(len(counts), dtype=np.int32), counts))
+    return s
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_tiles_of_a_row_or_two_over_many_columns(dtype):
+    # tiles whose rows one warp brings, or whose base none does, while the stages turn many times: every run the same
+    # and none gives up
+    counts, d, N, R = [6000, 1, 129, 5, 0, 33], 4104, 2056, 128
+    rows, n = sum(counts), len(counts)
+    s = _ragged(counts, d, N, R, seed=21)
+    x, A, B, base, dC = _gpu(s, "x", "A", "B", "base", "dC")
+    off, order = _plan(s, n)
+    L = gg.lib()
+    assert L.moe_lora_workspace_size(rows, n, d, N, R) > 0
+    f = torch.empty(L.moe_lora_workspace_size(rows, n, d, N, R), dtype=torch.uint8, device=DEV)
+    b = torch.empty(L.moe_lora_backward_workspace_size(rows, n, d, N, R), dtype=torch.uint8, device=DEV)
+    h = torch.randn(rows, R, generator=torch.Generator(DEV).manual_seed(1), device=DEV)
+    first = None
+    for _ in range(20):
+        got = [gg.lora(x, A, B, off, order, out_dtype=dtype, ws=f),
+               gg.lora(x, A, B, off, order, base=base.to(dtype), ws=f),
+               *gg.lora_backward(dC, x, h, A, B, off, order, dx_dtype=dtype, ws=b),
+               gg.lora_backward(dC, x, h, A, B, off, order, dx_dtype=dtype, want_grads=False, ws=b)[0]]
+        assert gg.read_device_status(f) == 0 and gg.read_device_status(b) == 0
+        first = first or got
+        assert all(torch.equal(u, v) for u, v in zip(first, got))
+    assert torch.equal(got[2], got[5])
+    _check_forward(s, got[0], None, None, None)
+    _check_forward(s, got[1], None, None, s["base"].to(dtype))
+    _check_backward(s, got[2:5], h.cpu(), None, None)
