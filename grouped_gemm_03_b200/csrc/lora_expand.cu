@@ -183,12 +183,11 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandCfg<RP, KN, OT>::PER_SM)
         gather4_once(dst + sub * (kRows * 128) + quad * 512, &map_base, &full[t % S], col + sub * (128 / sizeof(OT)), row,
                      policy);
     }
-    if (blocks <= S) load_h();
-    if (!ok) {   // what is in flight lands before the block ends
-      int never = 0;
-      for (int u = t > S ? t - S : 0; u < t; ++u) ptx::mbar_wait_warp(&full[u % S], (u / S) & 1, &never, kWaitLimitNs);
-      ptx::mbar_wait_warp(&h_full, 0, &never, kWaitLimitNs);
-    }
+    if (ok && blocks <= S) load_h();
+    // what is in flight lands before the block ends, whoever gave up
+    int never = 0;
+    for (int u = t > S ? t - S : 0; u < t; ++u) ptx::mbar_wait_warp(&full[u % S], (u / S) & 1, &never, kWaitLimitNs);
+    if (warp == 0) ptx::mbar_wait_warp(&h_full, 0, &never, kWaitLimitNs);
   } else if (warp < kMmaWarp) {
     // ---- block by block: accumulator + base, out
     const int ew = warp - kLoaders / 32, quarter = ew & 3, half = ew >> 2;

@@ -178,7 +178,6 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
   }
   const int blocks = max(0, min(p.cols, W - col0) + kTile - 1) / kTile;  // none behind the last column
   const int steps = (end - start + kTile - 1) / kTile;
-  const int tiles = steps * blocks;
   const bool want_p = PROJ && (!GRAD || p.proj), want_g = GRAD && p.grad;
 
   __syncthreads();
@@ -276,10 +275,9 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
         }
       }
     }
-    if (!ok) {   // what is in flight lands before the block ends
-      int never = 0;
-      for (int u = t > S ? t - S : 0; u < t; ++u) ptx::mbar_wait_warp(&full[u % S], (u / S) & 1, &never, kWaitLimitNs);
-    }
+    // what is in flight lands before the block ends, whoever gave up
+    int never = 0;
+    for (int u = t > S ? t - S : 0; u < t; ++u) ptx::mbar_wait_warp(&full[u % S], (u / S) & 1, &never, kWaitLimitNs);
   } else if (warp < kMmaWarp) {
     // ---- P out, and at the end G.  Two warps to a quarter of TMEM's lanes, half the columns each.
     const int et = tid - kLoaders, ew = warp - kLoaders / 32, quarter = ew & 3, half = ew >> 2;
@@ -452,11 +450,9 @@ __global__ void __launch_bounds__(StreamCfg<RP, PROJ, GRAD>::THREADS, StreamCfg<
       if (ok) ptx::umma_commit(&step_done[step & 1]);
     }
     ptx::umma_commit(&drained);
-    if (!ok) {
-      give_up();
-      int never = 0;   // what was issued is waited for before TMEM goes
-      ptx::mbar_wait(&drained, 0, &never, kWaitLimitNs);
-    }
+    if (!ok) give_up();
+    int never = 0;   // what was issued, arrivals too, is waited for before TMEM and the block go
+    ptx::mbar_wait(&drained, 0, &never, kWaitLimitNs);
   }
   __syncwarp();
   __syncthreads();
