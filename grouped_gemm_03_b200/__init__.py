@@ -342,7 +342,9 @@ def combine_backward(dout, Y, token_to_row, topk_w, has_shared: bool, offsets=No
     """(dY [R', d] bf16, d_topk_w [T, k] fp32) of combine's output gradient (moe_combine_backward).
 
     offsets: the permute's, for a plan with a capacity.  Either result can be left out (None); Y may be
-    None without d_topk_w.  Rows of dY that belong to no token are left as they were (a new dY's are 0)."""
+    None without d_topk_w.  Rows of dY that belong to no token are left as they were; a new dY's are 0 where
+    offsets are given.  Without them a new dY is not cleared first (that would cost a third of the call): every row
+    has to be a slot's, as moe_permute's plan has it.  For another plan, one with slots of -1, give a zeroed dY."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return combine_backward(dout, Y, token_to_row, topk_w, has_shared, offsets, want_dY, want_dw, dY)

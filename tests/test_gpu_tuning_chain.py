@@ -142,3 +142,28 @@ def test_a_fine_tuning_step():
     near(dA, A64.grad)
     near(dB, B64.grad)
     assert torch.isfinite(dH).all()
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_combine_backward_of_slots_without_a_row(shared):
+    # a caller's own plan: slots of -1 without the permute's offsets, into a dY that the caller has cleared
+    T, d, k = 40, 136, 3
+    r = np.random.default_rng(8)
+    rows = T * k + (T if shared else 0)
+    t2r = r.permutation(T * k).reshape(T, k).astype(np.int32)
+    lost = [(0, 0), (3, 2), (7, 0), (7, 1), (7, 2), (39, 1)]
+    gone = [int(t2r[at]) for at in lost]
+    for at in lost:
+        t2r[at] = -1
+    Y = torch.from_numpy(r.normal(size=(rows, d))).to(torch.bfloat16)
+    Y[gone] = float("nan")
+    dout = torch.from_numpy(r.normal(size=(T, d))).to(torch.bfloat16)
+    w = torch.from_numpy(r.random(size=(T, k)).astype(np.float32))
+    w[3, 2] = float("nan")
+    wY, ww = tuning.combine_backward(dout, Y, t2r, w, T * k if shared else None)
+    dY = torch.zeros(rows, d, dtype=torch.bfloat16, device=DEV)
+    got, dw = gg.combine_backward(dout.to(DEV), Y.to(DEV), torch.from_numpy(t2r).to(DEV), w.to(DEV), shared, dY=dY)
+    assert got is dY and not dY[gone].any()
+    assert np.all(np.abs(as_f64(dY) - wY) <= (2.0 ** -8 + 2.0 ** -23) * np.abs(wY))
+    mag = tuning.combine_backward(dout.abs(), Y.nan_to_num().abs(), t2r, w, None)[1]
+    assert np.all(np.abs(as_f64(dw) - ww) <= (d / 32 + 16) * 2.0 ** -24 * mag)
