@@ -22,7 +22,10 @@
 // h enters the second product as two bf16 terms (hi + lo, 16 bits of mantissa
 // together) for a bf16 result and as three (all 24) for an fp32 one: one bf16
 // term alone would put its own rounding, 2^-9 a value, beside that of a bf16
-// result, and two left 1e-6 of an fp32 one.
+// result, and two left 1e-6 of an fp32 one.  base joins the product's sum at its
+// end, in fp32: as the accumulator it would be cut off at its own size in every
+// one of up to 24 steps (beside a base of 2^12 an fp32 result left the bound of
+// its one rounding at every rank; the time is the same either way).
 #include <cstdint>
 
 #include "common.cuh"
@@ -329,11 +332,9 @@ __global__ void __launch_bounds__(kLoraThreads, RP <= 64 ? 2 : 1) lora_kernel(co
     const bool in = nb + c * 8 < n1;
     float acc[4][4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int t = 0; t < 4; ++t) acc[t][2 * h] = v[h][2 * t], acc[t][2 * h + 1] = v[h][2 * t + 1];
-#pragma unroll
     for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
       uint32_t bt[RP / 16][2];
       if constexpr (kAhead) {
 #pragma unroll
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP <= 64 ? 2 : 1) lora_kernel(co
       if (!in || !rl[h]) continue;
       float o[8];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) o[2 * t] = acc[t][2 * h], o[2 * t + 1] = acc[t][2 * h + 1];
+      for (int t = 0; t < 4; ++t) o[2 * t] = v[h][2 * t] + acc[t][2 * h], o[2 * t + 1] = v[h][2 * t + 1] + acc[t][2 * h + 1];
       store8(out + ro[h] + nb, o);
     }
   }

@@ -457,3 +457,27 @@ def test_tiles_of_a_row_or_two_over_many_columns(dtype):
     _check_forward(s, got[0], None, None, None)
     _check_forward(s, got[1], None, None, s["base"].to(dtype))
     _check_backward(s, got[2:5], h.cpu(), None, None)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,n,d,N,R", [(61, 5, 264, 200, 8), (200, 3, 136, 264, 40), (333, 4, 96, 96, 64), (150, 2, 72, 136, 128),
+                                          (12500, 5, 520, 504, 64), (6100, 3, 256, 264, 104)])
+def test_base_is_added_once(rows, n, d, N, R, dtype):
+    """base is no part of the product's sums: beside a base of 2^12 the result is off by its one rounding and, far
+    below that, by the product's own bound (_check_forward's, without base in the sums)."""
+    s = _inputs(rows, n, d, N, R, seed=R + 1)
+    base = (s["base"].float() * 4096).to(dtype)
+    if dtype == torch.float32:   # all 24 bits in use
+        base += torch.from_numpy(np.random.default_rng(2).uniform(-1, 1, size=base.shape).astype(np.float32))
+    x, A, B, scale = _gpu(s, "x", "A", "B", "scale")
+    off, order = _plan(s, n)
+    out = gg.lora(x, A, B, off, order, scale=scale, base=base.to(DEV))
+    want, wh = tuning.lora(s["x"], s["A"], s["B"], s["row"], s["scale"], base)
+    mag, magh = tuning.lora(*(np.abs(as_f64(s[v])) for v in ("x", "A", "B")), s["row"], s["scale"].abs())
+    tol = np.zeros_like(want)
+    for a in range(n):
+        r = np.nonzero(s["row"] == a)[0]
+        e = depth(d) * magh[r] + (SPLIT + 2.0 ** -23) * np.abs(wh[r]) + depth(2 * R) * np.abs(wh[r])
+        tol[r] = abs(float(s["scale"][a])) * (e @ np.abs(as_f64(s["B"][a])).T)
+    once = STEP[dtype] + (2.0 ** -24 if dtype == torch.bfloat16 else 0)   # the fp32 sum before a bf16 rounding
+    _close(out, want, tol + once * (np.abs(want) + tol), "out")
