@@ -157,6 +157,7 @@ struct LoraArgs {
   const void* base;
   void* out;
   float* h_out;
+  int* status;          // nullptr: the caller has no workspace
   int kslice, nslice;   // columns of x / of out a CTA of the cluster takes, multiples of 32
 };
 
@@ -189,6 +190,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP <= 64 ? 2 : 1) lora_kernel(co
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;
   int a, start, end;
+  if (p.status && blockIdx.x == 0 && tid == 0) *p.status = MOE_OK;   // no wait here can run out
   if (!find_tile<MT>(p.offsets, p.n, p.rows, blockIdx.x / CS, a, start, end)) return;  // the whole cluster leaves
   if (tid < MT) {
     int r = start + tid < end ? p.order[start + tid] : -1;
@@ -434,9 +436,12 @@ size_t lora_workspace_bytes(int rows, int n, int d, int N, int R) {
 }
 
 int launch_lora(const LoraForwardArgs& q, cudaStream_t s) {
-  if (q.rows == 0) return MOE_OK;
+  int* status = static_cast<int*>(q.ws);
+  if (q.rows == 0) {
+    if (status) MOE_CUDA_CHECK(cudaMemsetAsync(status, 0, sizeof(int), s));   // MOE_OK
+    return MOE_OK;
+  }
   if (lora_two_launches(q.rows, q.n, q.d, q.N, q.R)) {
-    int* status = static_cast<int*>(q.ws);
     uint8_t* h = static_cast<uint8_t*>(q.ws) + 256;
     StreamArgs p{};
     p.X = static_cast<const __nv_bfloat16*>(q.x), p.M = static_cast<const __nv_bfloat16*>(q.A);
@@ -459,6 +464,7 @@ int launch_lora(const LoraForwardArgs& q, cudaStream_t s) {
   p.x = static_cast<const __nv_bfloat16*>(q.x), p.A = static_cast<const __nv_bfloat16*>(q.A);
   p.B = static_cast<const __nv_bfloat16*>(q.B), p.scale = q.scale, p.offsets = q.offsets, p.order = q.order;
   p.n = q.n, p.rows = q.rows, p.d = q.d, p.N = q.N, p.R = q.R, p.base = q.base, p.out = q.out, p.h_out = q.h_out;
+  p.status = status;
   return q.out_dtype == MOE_F32 ? launch_lora_rank<float>(p, s) : launch_lora_rank<__nv_bfloat16>(p, s);
 }
 

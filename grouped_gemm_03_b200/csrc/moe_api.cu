@@ -497,6 +497,7 @@ int moe_lora(const void* x, const void* A, const void* B, const float* scale, co
     return MOE_ERR_INVALID;
   const size_t need = lora_workspace_bytes(rows, n, d, N, R);
   if (need > 0 && (!ws || !aligned(ws, 256) || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (!aligned(ws, 256) || ws_bytes < 256) ws = nullptr;   // not needed, and no place for a status word
   LoraForwardArgs a{};
   a.x = x, a.A = A, a.B = B, a.scale = scale, a.offsets = offsets, a.order = order;
   a.n = n, a.rows = rows, a.d = d, a.N = N, a.R = R;

@@ -394,7 +394,8 @@ int moe_adapter_plan(const int32_t* row_adapter, int rows, int n, int32_t* offse
  *          rows without an adapter are then not touched
  *   h_out  [rows, R] fp32: x A^T (0 for rows without an adapter), which
  *          moe_lora_backward takes, or NULL
- *   ws     moe_lora_workspace_size(...) bytes (status + h); where that is 0, NULL
+ *   ws     moe_lora_workspace_size(...) bytes (status + h); where that is 0, NULL, or a
+ *          workspace of 256 bytes or more for the status word alone
  * fp32 sums, rounded once to out_dtype.  Status word (where there is a
  * workspace): MOE_ERR_TIMEOUT.  R a multiple of 8, 8 <= R <= 128
  * (pad smaller ranks with zeros); d % 8 == 0, N % 8 == 0, both <= 2^20; x, A, B,

@@ -481,3 +481,22 @@ def test_base_is_added_once(rows, n, d, N, R, dtype):
         tol[r] = abs(float(s["scale"][a])) * (e @ np.abs(as_f64(s["B"][a])).T)
     once = STEP[dtype] + (2.0 ** -24 if dtype == torch.bfloat16 else 0)   # the fp32 sum before a bf16 rounding
     _close(out, want, tol + once * (np.abs(want) + tol), "out")
+
+
+@pytest.mark.parametrize("rows", [0, 30, 12500])
+def test_a_callers_workspace_has_the_calls_status(rows):
+    # one workspace for batches of any size: whatever an earlier call left, the status is this call's
+    n, d, N, R = 5, 520, 504, 64
+    s = _inputs(rows, n, d, N, R, seed=31)
+    x, A, B = _gpu(s, "x", "A", "B")
+    off, order = _plan(s, n)
+    ws = torch.empty(gg.lib().moe_lora_workspace_size(12500, n, d, N, R), dtype=torch.uint8, device=DEV)
+    ws.fill_(0xff)
+    out = gg.lora(x, A, B, off, order, ws=ws)
+    assert gg.read_device_status(ws) == 0
+    assert torch.equal(out, gg.lora(x, A, B, off, order))
+    if rows < 12500:   # where none is needed, one without room for a status word is left alone
+        for short in (ws[:128], ws[64:1024]):
+            ws.fill_(0xff)
+            gg.lora(x, A, B, off, order, ws=short)
+            assert (ws == 0xff).all()
