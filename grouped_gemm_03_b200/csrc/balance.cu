@@ -459,6 +459,8 @@ __device__ void balance_finish(const BalanceArgs& a, int cols, int w) {
   if (rank == 0) {
     int err = 0;
     for (int i = tid; i < a.chunks; i += NT) err |= a.part_err[i];
+    if (a.T == 0 && a.off)   // no first pass to look at the offsets: all of them are 0
+      for (int i = tid; i <= a.S; i += NT) err |= a.off[i] != 0 ? 2 : 0;
     const int bad = __syncthreads_or(err & 2), odd = __syncthreads_or(err & 1);
     if (tid == 0) {
       float all = 0.f;

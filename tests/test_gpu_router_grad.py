@@ -299,3 +299,14 @@ def test_large_finite_rows(T, E, dtype):
         sel = np.take_along_axis(p, idx, 1).sum(1, keepdims=True) if renorm else 1.0
         G = np.abs(g).max(1, keepdims=True) / sel + coef.max() * counts.max()
         _check_grad(d, want, p, G, renorm_extra=1.0 if renorm else 0.0)
+
+
+@pytest.mark.parametrize("offsets,status", [([0, 0, 0], 0), ([0, 0, 5], -5), ([0, -1, 0], -5), ([2, 0, 0], -5), ([0, 3, 0], -5)])
+def test_offsets_of_no_tokens(offsets, status):
+    e = torch.empty
+    ws = e(gg.lib().moe_balance_loss_workspace_size(0, 8, 2), dtype=torch.uint8, device=DEV)
+    ws.fill_(0xff)
+    loss, counts, prob, coef = gg.balance_loss(e(0, 8, device=DEV), e(0, 2, dtype=torch.int32, device=DEV), 1.0,
+                                               _dev(np.array(offsets), torch.int32), ws=ws)
+    assert gg.read_device_status(ws) == status
+    assert loss.item() == 0 and not counts.any() and not prob.any() and not coef.any()
