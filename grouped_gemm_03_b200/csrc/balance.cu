@@ -879,7 +879,8 @@ int launch_router_backward(const void* logits, int dtype, const int32_t* idx, co
   RouterGradArgs a{};
   const int V = values_for(E);
   a.logits = logits, a.idx = idx, a.d_w = d_w, a.T = T, a.E = E, a.k = k, a.renorm = renorm, a.off = off, a.S = S;
-  a.mask = mask, a.counts = counts, a.coef = coef, a.d_loss = d_loss, a.out = out;
+  a.mask = counts ? mask : nullptr;   // a token's gates have their gradient whether it counts or not
+  a.counts = counts, a.coef = coef, a.d_loss = d_loss, a.out = out;
   a.L = lanes_for(E, V);
   while (a.L * 2 < k) a.L *= 2;   // two slots to a lane
   a.vec = E % (dtype == MOE_F32 ? 4 : 8) != 0 ? 0 : E == a.L * V ? 2 : 1;   // not 0: rows of every output type are stored whole too

@@ -310,3 +310,19 @@ def test_offsets_of_no_tokens(offsets, status):
                                                _dev(np.array(offsets), torch.int32), ws=ws)
     assert gg.read_device_status(ws) == status
     assert loss.item() == 0 and not counts.any() and not prob.any() and not coef.any()
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+def test_a_mask_is_the_losss_alone(renorm):
+    # without the loss's counts, mask and offsets change nothing; with them, the gates' part of a masked token stays
+    T, E, k = 90, 40, 4
+    logits, idx, offsets, mask = _inputs(T, E, k, 3, torch.float32, True, seed=13)
+    g = torch.randn(T, k, generator=torch.Generator().manual_seed(4)).to(DEV)
+    args = _dev(logits), _dev(idx), g, renorm
+    plain = gg.router_backward(*args)
+    assert torch.equal(plain, gg.router_backward(*args, mask=_dev(mask), seq_offsets=_dev(offsets, torch.int32)))
+    _, counts, _, coef = gg.balance_loss(_dev(logits), _dev(idx), 1.0, _dev(offsets, torch.int32), _dev(mask))
+    both = gg.router_backward(*args, counts=counts, coef=coef, mask=_dev(mask), seq_offsets=_dev(offsets, torch.int32))
+    dead = torch.from_numpy(mask == 0).to(DEV)
+    dead[int(offsets[-1]):] = True
+    assert torch.equal(both[dead], plain[dead]) and not torch.equal(both, plain)
