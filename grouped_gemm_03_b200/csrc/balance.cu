@@ -605,6 +605,10 @@ struct RouterGradArgs {
   int chunk, L, vec;
 };
 
+// Selected mass below which a renormalised row is worked out again: a probability that underflowed is then less
+// than 1e-18 of it.
+constexpr float kLowMass = 1e-20f;
+
 // The dense part of a row, p (bal - dot), is written in whole pieces; the
 // selected experts' entries are then written over it by the lanes that hold
 // the slots (lane l slots l and l + L), which read their own logit again: a
@@ -732,10 +736,31 @@ __global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 2) router_backward_
         }
       }
     }
-    float inv_z = 0.f;
+    float inv_z = 0.f, pw[U];   // the renormalised gates' numerators: the selected probabilities
+#pragma unroll
+    for (int u = 0; u < U; ++u) pw[u] = gates ? ps[u] : 0.f;
     if (kRenorm && gates) {   // over the selected experts alone: w = p / z, their gradient w (g - sum w g)
       z = group_sum(z, L);
       wg = group_sum(wg, L);
+      // Selected experts far below the row's maximum (chosen by something else than these logits): their masses
+      // underflow, so their softmax is taken from their own maximum.
+      const bool low = any && z < kLowMass;
+      if (__any_sync(0xffffffffu, low)) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < U; ++u) top = fmaxf(top, x[u]);   // -inf where there is none
+        top = group_max(top, L);
+        float zl = 0.f, wl = 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float pu = low && x[u] > -INFINITY ? exp_from(x[u], top) : 0.f;
+          if (low) pw[u] = pu;
+          zl += pu, wl += e[u] >= 0 ? pu * g[u] : 0.f;
+        }
+        zl = group_sum(zl, L);
+        wl = group_sum(wl, L);
+        if (low) z = zl, wg = wl;
+      }
       inv_z = z == 0.f ? 0.f : __fdiv_rn(1.f, z);
       wg *= inv_z;
     }
@@ -766,7 +791,7 @@ __global__ void __launch_bounds__(kBalThreads, V <= 16 ? 3 : 2) router_backward_
         if (!live || !any || e[u] < 0) continue;
         float v;
         if (kRenorm)
-          v = fmaf(ps[u] * inv_z, gs[u] - ns[u] * wg, ps[u] * (be[u] - dot));
+          v = fmaf(pw[u] * inv_z, gs[u] - ns[u] * wg, ps[u] * (be[u] - dot));
         else
           v = ps[u] * (be[u] + gs[u] - dot);
         o[e[u]] = from_f32(v, OT());

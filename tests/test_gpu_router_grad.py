@@ -326,3 +326,24 @@ def test_a_mask_is_the_losss_alone(renorm):
     dead = torch.from_numpy(mask == 0).to(DEV)
     dead[int(offsets[-1]):] = True
     assert torch.equal(both[dead], plain[dead]) and not torch.equal(both, plain)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,k", [(16, 2), (24, 5), (256, 4), (96, 32), (1000, 8)])
+def test_renormalised_gates_far_below_the_row(E, k, dtype):
+    """Ids that something else than these logits chose: the selected experts' probabilities underflow in fp32, their
+    softmax among themselves does not.  w (g - sum w g) is then within a few EPS of max|g| (1 at most here)."""
+    T = 65
+    r = np.random.default_rng(E)
+    logits = torch.from_numpy(r.normal(size=(T, E))).to(dtype)
+    idx = np.stack([r.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    for t in range(0, T, 2):
+        logits[t, idx[t].astype(np.int64)] += (-40, -95, -130, -600)[t // 2 % 4]
+    idx[6, 1] = -1                                        # a slot without an expert
+    logits[8, int(idx[8, 0])] = float("-inf")             # one of the selected has none of the mass
+    logits[10, torch.from_numpy(idx[10]).long()] = float("-inf")   # nor has any
+    g = r.uniform(-1, 1, size=(T, k)).astype(np.float32)
+    got = gg.router_backward(_dev(logits), _dev(idx), _dev(g), True).cpu().numpy()
+    want = tuning.router_backward(logits, idx, g, True)
+    np.testing.assert_allclose(got, want, rtol=0, atol=20 * EPS)
+    assert (np.abs(want).max(1) > 1e-3).sum() >= T - 4   # of two slots, rows 6 and 8 keep one: no gradient, as row 10
