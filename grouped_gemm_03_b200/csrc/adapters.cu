@@ -372,7 +372,7 @@ int launch_lora_tiles(LoraArgs& p, cudaStream_t s) {
   // as many CTAs as are resident together: a second wave took 11.3 us where one takes 6.8 (61 rows of 48 adapters,
   // clusters of 8 against 4)
   const long long half_full = p.rows / MT + p.n / 2, one_each = p.n < p.rows ? p.n : p.rows;
-  static std::atomic<int> known[9] = {};
+  static KnownClusters known;
   const int cs = cluster_for(known, kernel, kLoraThreads, L::SMEM, half_full > one_each ? half_full : one_each,
                              p.d > p.N ? p.d : p.N);
   p.kslice = ((p.d + cs - 1) / cs + 31) / 32 * 32;

@@ -92,13 +92,18 @@ int allow_smem(std::atomic<uint64_t>& done, K kernel, int bytes) {
   return MOE_OK;
 }
 
-// How many clusters of `cs` CTAs of `kernel` are resident together (0: the runtime does not say); `known` (one
-// per kernel and size) holds the answer.  A cluster lies within one group of SMs: with two CTAs to an SM 148 pairs
-// fit, but only 71 fours and 33 eights.
+// What resident_clusters has been told, by device and cluster size: 0 not asked yet, else the answer + 1.
+struct KnownClusters {
+  std::atomic<int> at[64][9] = {};
+};
+
+// How many clusters of `cs` CTAs of `kernel` are resident together on device `dev` (0: none, or the runtime does not
+// say); `known` (one per kernel) holds the answers.  A cluster lies within one group of SMs: with two CTAs to an SM
+// 148 pairs fit, but only 71 fours and 33 eights.
 template <typename K>
-int resident_clusters(std::atomic<int>& known, K kernel, int threads, size_t smem, int cs) {
-  int n = known.load();
-  if (n > 0) return n;
+int resident_clusters(KnownClusters& known, int dev, K kernel, int threads, size_t smem, int cs) {
+  std::atomic<int>* at = dev >= 0 && dev < 64 ? &known.at[dev][cs] : nullptr;
+  if (const int told = at ? at->load() : 0) return told - 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cs);
   cfg.blockDim = dim3(threads);
@@ -110,11 +115,12 @@ int resident_clusters(std::atomic<int>& known, K kernel, int threads, size_t sme
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  int n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
     cudaGetLastError();   // an estimate only: the launch itself reports what is wrong
     n = 0;
   }
-  known.store(n);
+  if (at) at->store(n + 1);
   return n;
 }
 
@@ -123,9 +129,10 @@ int resident_clusters(std::atomic<int>& known, K kernel, int threads, size_t sme
 // second wave where they lay worse (1021 rows of 12 adapters, rank 64: 28 -> 22 us) and cost as much where they did
 // not (18 -> 21).
 template <typename K>
-int cluster_for(std::atomic<int> (&known)[9], K kernel, int threads, size_t smem, long long tiles, int widest) {
-  int cs = 1;
-  while (cs < 8 && widest >= (cs + 1) * 128 && tiles <= resident_clusters(known[cs + 1], kernel, threads, smem, cs + 1)) ++cs;
+int cluster_for(KnownClusters& known, K kernel, int threads, size_t smem, long long tiles, int widest) {
+  int cs = 1, dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
+  while (cs < 8 && widest >= (cs + 1) * 128 && tiles <= resident_clusters(known, dev, kernel, threads, smem, cs + 1)) ++cs;
   return cs;
 }
 

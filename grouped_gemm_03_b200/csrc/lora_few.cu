@@ -312,7 +312,7 @@ int launch_few(const LoraBackwardArgs& q, FewParts w, cudaStream_t s) {
   const int st = allow_smem(done, kernel, F::SMEM);
   if (st != MOE_OK) return st;
   const long long half_full = q.rows / kRowsFew + q.n / 2, one_each = q.n < q.rows ? q.n : q.rows;
-  static std::atomic<int> known[9] = {};
+  static KnownClusters known;
   const int cs = cluster_for(known, kernel, kFewThreads, F::SMEM, half_full > one_each ? half_full : one_each,
                              q.d > q.N ? q.d : q.N);
   w.kslice = ((q.d + cs - 1) / cs + 63) / 64 * 64;
