@@ -807,9 +807,9 @@ int lanes_for(int E, int V) {  // lanes of a row: a power of two, V columns each
 }
 int values_for(int E) { return E <= 512 ? 16 : 32; }
 
-// Blocks that run at once: three to an SM of 148, two where a lane holds 32 columns (with one, 8192 tokens of 1024
+// Blocks that run at once: three to an SM, two where a lane holds 32 columns (with one, 8192 tokens of 1024
 // experts in bf16 took the gradient 29.4 us in three waves, 18.8 in one of two to an SM).
-int blocks_at_once(int E) { return 148 * (values_for(E) == 16 ? 3 : 2); }
+int blocks_at_once(int E) { return num_sms() * (values_for(E) == 16 ? 3 : 2); }
 
 int balance_chunk(int T, int E) {
   if (T <= kBalSmall) return T > 0 ? (T + kFinCluster - 1) / kFinCluster : 1;
