@@ -95,31 +95,63 @@ struct GradReduceArgs {
   int n, rows;
 };
 
-// Adapter blockIdx.y's gradient blockIdx.z (0 dA, 1 dB): the sum over its
-// chunks.  That of a single one, or of none, is there already.
+// Gradient blockIdx.y (0 dA, 1 dB) of the adapters of more than one chunk: the
+// sum over the chunks.  That of a single one, or of none, is there already.
+// How many adapters have several and which is on the device, so every block
+// lists them and the blocks share their values out evenly: with a fixed share of
+// the blocks to an adapter, the sums of 4096 rows of one of 1024 adapters were
+// a single block's work (a call of rank 64 and 2048 and 2048 columns 7450 us,
+// 382 now, most of it the others' zeros; 8191 rows of 16 adapters 141 -> 127).
+constexpr int kReduceThreads = 256, kReducePiece = kReduceThreads * 4;
+
 template <typename GT>
-__global__ void __launch_bounds__(256) grad_reduce_kernel(const GradReduceArgs p) {
+__global__ void __launch_bounds__(kReduceThreads) grad_reduce_kernel(const GradReduceArgs p) {
   pdl_wait();
   pdl_launch_dependents();
-  const int a = blockIdx.y, z = blockIdx.z, chunk = p.chunk[z];
-  const int b = held_offset(p.offsets, p.n, p.rows, a), e = held_offset(p.offsets, p.n, p.rows, a + 1);
-  const int chunks = e > b ? (e - b + chunk - 1) / chunk : 0;
-  if (chunks <= 1 || !p.grad[z]) return;
+  __shared__ int s_adapter[kMaxAdapters];
+  __shared__ int s_found[kReduceThreads / 32];
+  const int z = blockIdx.y, chunk = p.chunk[z], tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (!p.grad[z]) return;
+  auto chunks_of = [&](int a, int& first) {
+    first = held_offset(p.offsets, p.n, p.rows, a);
+    const int last = held_offset(p.offsets, p.n, p.rows, a + 1);
+    return last > first ? (last - first + chunk - 1) / chunk : 0;
+  };
+  int found = 0, first;
+  for (int a0 = 0; a0 < p.n; a0 += kReduceThreads) {   // in ascending order, the same in every block
+    const bool several = a0 + tid < p.n && chunks_of(a0 + tid, first) > 1;
+    const unsigned in = __ballot_sync(0xffffffffu, several);
+    if (lane == 0) s_found[warp] = __popc(in);
+    __syncthreads();
+    int at = found;
+#pragma unroll
+    for (int w = 0; w < kReduceThreads / 32; ++w) {
+      at += w < warp ? s_found[w] : 0;
+      found += s_found[w];
+    }
+    if (several) s_adapter[at + __popc(in & ((1u << lane) - 1))] = a0 + tid;
+    __syncthreads();
+  }
   const size_t size = p.size[z];
-  const float* part = p.part[z] + part_slot(b, chunk) * size;
-  GT* grad = static_cast<GT*>(p.grad[z]) + a * size;
-  for (size_t i = (static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x) * 4; i < size;
-       i += static_cast<size_t>(gridDim.x) * blockDim.x * 4) {
+  const int pieces = static_cast<int>((size + kReducePiece - 1) / kReducePiece);
+  const long long all = static_cast<long long>(found) * pieces;
+  for (long long it = blockIdx.x; it < all; it += gridDim.x) {
+    const int a = s_adapter[it / pieces];
+    const size_t i = static_cast<size_t>(it % pieces) * kReducePiece + tid * 4;
+    if (i >= size) continue;
+    const int chunks = chunks_of(a, first);
+    const float* part = p.part[z] + part_slot(first, chunk) * size + i;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
     for (int s = 0; s < chunks; ++s) {
-      const float4 u = __ldcs(reinterpret_cast<const float4*>(part + s * size + i));
+      const float4 u = __ldcs(reinterpret_cast<const float4*>(part + s * size));
       v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
     }
+    GT* grad = static_cast<GT*>(p.grad[z]) + a * size + i;
     if constexpr (sizeof(GT) == 4)
-      *reinterpret_cast<float4*>(grad + i) = v;
+      *reinterpret_cast<float4*>(grad) = v;
     else
-      *reinterpret_cast<uint2*>(grad + i) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+      *reinterpret_cast<uint2*>(grad) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
   }
 }
 
@@ -272,11 +304,17 @@ int launch_lora_backward(const LoraBackwardArgs& q, cudaStream_t s) {
   r.size[0] = sizeA, r.size[1] = sizeB;
   r.chunk[0] = L.x.chunk, r.chunk[1] = L.dc.chunk;
   r.offsets = q.offsets, r.n = q.n, r.rows = q.rows;
-  // four blocks to an SM over all the adapters, no more than one pass needs
-  const size_t need = (r.size[0] > r.size[1] ? r.size[0] : r.size[1]) / 1024 + 1, share = 4ul * num_sms() / q.n + 1;
-  const dim3 grid(static_cast<unsigned>(need < share ? need : share), q.n, 2);
+  // four blocks to an SM, no more than there can be pieces
+  size_t most = 1;
+  for (int z = 0; z < 2; ++z) {
+    const size_t several = static_cast<size_t>(q.rows) / (r.chunk[z] + 1), held = q.n;
+    const size_t pieces = (several < held ? several : held) * ((r.size[z] + kReducePiece - 1) / kReducePiece);
+    if (r.grad[z] && pieces > most) most = pieces;
+  }
+  const size_t share = 4ul * num_sms();
+  const dim3 grid(static_cast<unsigned>(most < share ? most : share), 2);
   return launch_pdl("grad_reduce_kernel", q.grad_dtype == MOE_F32 ? grad_reduce_kernel<float> : grad_reduce_kernel<__nv_bfloat16>,
-                    grid, dim3(256), 0, s, r);
+                    grid, dim3(kReduceThreads), 0, s, r);
 }
 
 }  // namespace moe

@@ -500,3 +500,20 @@ def test_a_callers_workspace_has_the_calls_status(rows):
             ws.fill_(0xff)
             gg.lora(x, A, B, off, order, ws=short)
             assert (ws == 0xff).all()
+
+
+@pytest.mark.parametrize("rows,n,d,N,R,only", [(4000, 1024, 72, 136, 16, [700, 700, 700, 3]), (700, 300, 136, 72, 24, [299]),
+                                               (3000, 600, 64, 264, 8, [0, 255, 256, 257, 511, 512, 599]), (2600, 1000, 40, 72, 64, [31, 32])])
+def test_few_of_many_held_adapters(rows, n, d, N, R, only):
+    # a server holds many adapters, the batch uses a few: several partial sums of some, none of most
+    s = _inputs(rows, n, d, N, R, seed=n, only=only)
+    x, A, B, scale, dC, dx_base = _gpu(s, "x", "A", "B", "scale", "dC", "dx_base")
+    off, order = _plan(s, n)
+    out, h = gg.lora(x, A, B, off, order, scale=scale, out_dtype=torch.float32, want_h=True)
+    _check_forward(s, out, h, s["scale"], None)
+    for dtype in (torch.float32, torch.bfloat16):
+        got = gg.lora_backward(dC, x, h, A, B, off, order, scale=scale, dx_base=dx_base, grad_dtype=dtype)
+        _check_backward(s, got, h.cpu(), s["scale"], s["dx_base"])
+        rest = torch.ones(n, dtype=torch.bool, device=DEV)
+        rest[only] = False
+        assert not got[1][rest].any() and not got[2][rest].any()
