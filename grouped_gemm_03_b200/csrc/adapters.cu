@@ -423,6 +423,9 @@ int launch_adapter_plan(const int32_t* adapter, int rows, int n, int32_t* offset
 //   rank 32:  4096 of 16 35.2 / 44.2, 8192 of 8 (7168 columns in) 79.9 / 59.8
 //   rank 64:  256 of 8 12.8 / 15.4, 2048 of 4 27.6 / 29.0, 4096 of 4 47.3 / 34.7, 8192 of 32 92.8 / 61.5
 //   rank 128: 256 of 4 16.3 / 15.8, 1024 of 16 52.6 / 36.2
+// n is taken for the adapters in use, which the host does not know.  Where most
+// of those held are not, one launch serves as well (4096 rows, columns 2048 and
+// 2048, rank 64): of 1 in use and held 24.2 / 23.1, of 1 in 1024 held 24.8 / 48.7.
 bool lora_two_launches(int rows, int n, int d, int N, int R) {
   const double ns_per_hbm_byte = 1 / 6400.0, row = 2.0 * d + 4.0 * N, weights = 2.0 * R * (d + N);
   const double active = n < rows ? n : rows, tiles = rows / 16.0 + 0.5 * active;

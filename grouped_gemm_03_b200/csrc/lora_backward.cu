@@ -101,7 +101,7 @@ struct GradReduceArgs {
 // lists them and the blocks share their values out evenly: with a fixed share of
 // the blocks to an adapter, the sums of 4096 rows of one of 1024 adapters were
 // a single block's work (a call of rank 64 and 2048 and 2048 columns 7450 us,
-// 382 now, most of it the others' zeros; 8191 rows of 16 adapters 141 -> 127).
+// 382 now, most of it the others' zeros; 8191 rows of 16 adapters 138 -> 129).
 constexpr int kReduceThreads = 256, kReducePiece = kReduceThreads * 4;
 
 template <typename GT>
@@ -192,14 +192,27 @@ Split split_for(int rows, int n, int W, int R, bool proj) {
   return best;
 }
 
-// Whether one launch on tiles of few rows does it all (lora_few.cu): with up to
-// four rows to an adapter, and above rank 32 from eight adapters on.  Measured,
-// that launch against the streaming passes, columns 4096 and 4096:
-//   rank 16: 1 row of 1 adapter 9.1 / 13.9 us, 4 of 1 9.3 / 13.9, 8 of 1 15.5 / 14.4, 30 of 30 15.5 / 34.8,
-//            500 of 128 94 / 114, 64 of 8 21.4 / 21.3, 500 of 64 64.8 / 64.6
-//   rank 64: 2 of 1 22.3 / 16.2, 8 of 8 22.7 / 30.9, 32 of 32 41 / 91, 64 of 8 54 / 28, 500 of 64 172 / 159
-// and of 2048 columns at rank 64 100 of 100 61 / 145, at rank 128 131 / 188.
-bool few_rows(int rows, int n, int R) { return rows <= 4ll * n && (R <= 32 || n >= 8); }
+// Whether one launch on tiles of few rows does it all (lora_few.cu), by the mean
+// of rows to an adapter.  A tile of more than four rows costs that launch four
+// times the multiply-adds of one with up to four, so what a mean may be depends
+// on how much of the time those take (the rank) and on whether such a tile finds
+// others beside it (the adapters).  Measured, that launch against the streaming
+// passes, us; "spread": the rows lie at random over the adapters, else evenly;
+// columns 2048 and 2048, at ranks 16 and 32 with up to 32 adapters 4096 and 4096:
+//   rank 16, mean 1 / 2 / 4: of 2 adapters 9/16 9/16 10/16 (spread 15/16), of 8 9/26 9/22 17/22 (19/22), of 32 16/39
+//            16/39 17/40 (25/40), of 100 40/91 41/92 44/92 (84/91)
+//   rank 32, mean 2 / 4: of 4 14/20 14/18 (23/18), of 8 14/24 18/24 (27/24), of 32 24/51 25/52 (39/52),
+//            of 100 38/70 39/70 (70/70)
+//   rank 64, spread, mean 1 / 2 / 3 / 4: of 4 20/17 20/17 30/18 30/18, of 8 20/23 20/23 32/24 35/22, of 16 24/30 33/28
+//            37/29 42/29, of 24 27/38 29/44 42/45 44/45, of 32 28/48 38/51 44/52 47/53, of 100 85/106 92/123 102/130
+//            113/132, of 200 159/193 176/230 207/244 214/248
+//   rank 128, spread, mean 1 / 2: of 4 28/21 28/22, of 8 29/27 29/28, of 16 34/38 53/38, of 32 42/67 60/72, of 48 70/82
+//            110/98, of 64 74/107 112/129, of 100 205/150 206/173 (evenly 131/189 132/189), of 200 215/276 332/327
+bool few_rows(int rows, int n, int R) {
+  if (R <= 32) return rows <= 4ll * n;
+  if (R <= 64) return n >= 8 && rows <= (n >= 24 ? 4ll : 2ll) * n;
+  return n >= 8 && rows <= n;
+}
 
 struct BackwardLayout {
   bool few;

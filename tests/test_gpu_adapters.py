@@ -517,3 +517,18 @@ def test_few_of_many_held_adapters(rows, n, d, N, R, only):
         rest = torch.ones(n, dtype=torch.bool, device=DEV)
         rest[only] = False
         assert not got[1][rest].any() and not got[2][rest].any()
+
+
+# both sides of the rule that chooses one launch: the same sizes, a row more or less
+@pytest.mark.parametrize("rows,n,d,N,R,only", [(12, 3, 136, 72, 32, None), (13, 3, 136, 72, 32, None), (16, 8, 72, 136, 64, None),
+                                               (17, 8, 72, 136, 64, None), (96, 24, 64, 264, 40, None), (97, 24, 64, 264, 40, None),
+                                               (14, 7, 72, 64, 64, None), (8, 8, 136, 264, 128, None), (9, 8, 136, 264, 128, None),
+                                               (130, 130, 136, 264, 104, [0, 0, 5, 129]), (131, 130, 136, 264, 104, [0, 0, 5, 129])])
+def test_both_ways_of_few_rows(rows, n, d, N, R, only):
+    s = _inputs(rows, n, d, N, R, seed=rows + n, only=only)
+    h = torch.from_numpy(np.random.default_rng(7).normal(size=(rows, R)).astype(np.float32))
+    dC, x, A, B, scale, base = _gpu(s, "dC", "x", "A", "B", "scale", "dx_base")
+    off, order = _plan(s, n)
+    for dtype in (torch.float32, torch.bfloat16):
+        got = gg.lora_backward(dC, x, h.to(DEV), A, B, off, order, scale=scale, dx_base=base, grad_dtype=dtype)
+        _check_backward(s, got, h, s["scale"], s["dx_base"])
