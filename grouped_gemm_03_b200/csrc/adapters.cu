@@ -345,9 +345,9 @@ __global__ void __launch_bounds__(kLoraThreads, RP <= 64 ? 2 : 1) lora_kernel(co
         load_b_row<RP>(Bc + static_cast<size_t>(nb + 2 * t) * p.R, nb + (g >> 1) * 8 < n1, p.R, c, bt);
       }
 #pragma unroll
-      for (int k = 0; k < RP / 16; ++k)
+      for (int q = TERMS - 1; q >= 0; --q)   // the small terms first: only the largest's steps cut a whole sum off
 #pragma unroll
-        for (int q = TERMS - 1; q >= 0; --q)   // the small terms first
+        for (int k = 0; k < RP / 16; ++k)
           mma16816(acc[t], hf[q][k][0], hf[q][k][1], hf[q][k][2], hf[q][k][3], bt[k][0], bt[k][1]);
     }
 #pragma unroll
