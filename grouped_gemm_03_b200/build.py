@@ -1,7 +1,9 @@
 """Build libmoe.so (the C-ABI library) in-tree with nvcc for sm_100a, and _ops.so
-beside it, the compiled part of the Python binding (g++, PyTorch's headers).
+beside it, the compiled part of the Python binding (g++, PyTorch's headers; left
+out where PyTorch is not installed, and built again when it is another one).
 
     python -m grouped_gemm_03_b200.build [--force] [-v]
+    python grouped_gemm_03_b200/build.py                 # the same, without importing PyTorch for the C library
 
 Objects go to _build/ at the repository root; the shared library lands next
 to this file so the Python binding finds it.  cudart is linked statically, so
@@ -11,6 +13,8 @@ from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -87,9 +91,27 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     return LIB
 
 
+def _ops_made_for() -> str | None:
+    """What _ops.so is compiled against: PyTorch and Python, where PyTorch is there (None: it is not)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    return f"torch {importlib.metadata.version('torch')} at {spec.origin}, python {sys.version}"
+
+
 def _build_ops(force: bool, verbose: bool) -> None:
-    header = os.path.join(INCLUDE, "moe.h")
-    if not force and os.path.exists(OPS) and os.path.getmtime(OPS) >= max(map(os.path.getmtime, (OPS_SRC, header))):
+    header, stamp = os.path.join(INCLUDE, "moe.h"), os.path.join(BUILD, "ops.made_for")
+    made_for = _ops_made_for()
+    if made_for is None:   # the C library is complete without the Python binding
+        if verbose:
+            print("no PyTorch: _ops.so (the Python binding's compiled part) is not built", flush=True)
+        return
+    known = None
+    if os.path.exists(stamp):
+        with open(stamp) as f:
+            known = f.read()
+    if (not force and known == made_for and os.path.exists(OPS) and
+            os.path.getmtime(OPS) >= max(map(os.path.getmtime, (OPS_SRC, header)))):
         return
     import torch
 
@@ -108,6 +130,8 @@ def _build_ops(force: bool, verbose: bool) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {os.path.basename(OPS_SRC)}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, OPS)
+    with open(stamp, "w") as f:
+        f.write(made_for)
 
 
 def main(argv=None) -> int:
