@@ -532,3 +532,29 @@ def test_both_ways_of_few_rows(rows, n, d, N, R, only):
     for dtype in (torch.float32, torch.bfloat16):
         got = gg.lora_backward(dC, x, h.to(DEV), A, B, off, order, scale=scale, dx_base=base, grad_dtype=dtype)
         _check_backward(s, got, h, s["scale"], s["dx_base"])
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+@pytest.mark.parametrize("rows,n,d,N,R", [(30, 40, 136, 72, 16), (60, 40, 72, 136, 16), (900, 3, 264, 392, 40), (2600, 2, 136, 264, 24)])
+def test_each_result_alone(rows, n, d, N, R):
+    # the C call takes any of dx, dA, dB without the others: the same bits, and nothing else is written
+    s = _inputs(rows, n, d, N, R, seed=41, only=[0, 0, 0, 1, -1])
+    dC, x, A, B, scale, base = _gpu(s, "dC", "x", "A", "B", "scale", "dx_base")
+    h = torch.randn(rows, R, generator=torch.Generator(DEV).manual_seed(1), device=DEV)
+    off, order = _plan(s, n)
+    full = gg.lora_backward(dC, x, h, A, B, off, order, scale=scale, dx_base=base)
+    _check_backward(s, full, h.cpu(), s["scale"], s["dx_base"])
+    L = gg.lib()
+    ws = torch.empty(L.moe_lora_backward_workspace_size(rows, n, d, N, R), dtype=torch.uint8, device=DEV)
+    for wanted in range(1, 8):
+        got = [torch.full_like(t, 7.0) if wanted >> i & 1 else None for i, t in enumerate(full)]
+        ws.fill_(0xff)
+        st = L.moe_lora_backward(*map(_address, (dC, x, h, A, B, scale, off, order)), n, rows, d, N, R, _address(base),
+                                 _address(got[0]), 2, _address(got[1]), _address(got[2]), 0, ws.data_ptr(), ws.numel(),
+                                 torch.cuda.current_stream().cuda_stream)
+        assert st == 0 and gg.read_device_status(ws) == 0
+        for g, f in zip(got, full):
+            assert g is None or torch.equal(g, f), wanted

@@ -347,3 +347,40 @@ def test_renormalised_gates_far_below_the_row(E, k, dtype):
     want = tuning.router_backward(logits, idx, g, True)
     np.testing.assert_allclose(got, want, rtol=0, atol=20 * EPS)
     assert (np.abs(want).max(1) > 1e-3).sum() >= T - 4   # of two slots, rows 6 and 8 keep one: no gradient, as row 10
+
+
+@pytest.mark.parametrize("T,E,k,S", [(300, 24, 3, 5000), (1, 8, 2, 700), (900, 40, 2, 20000), (512, 1024, 8, 300)])
+def test_more_sequences_than_tokens(T, E, k, S):
+    logits, idx, offsets, mask = _inputs(T, E, k, S, torch.float32, T > 1, seed=S)
+    args = _dev(logits), _dev(idx), 0.5, _dev(offsets, torch.int32), _dev(mask)
+    got = gg.balance_loss(*args)
+    _check_loss(got, tuning.balance_loss(logits, idx, 0.5, offsets, mask))
+    bare = gg.balance_loss(*args, want_prob=False)
+    assert bare[2] is None and all(torch.equal(a, b) for a, b in zip(got, bare) if b is not None)
+    d = gg.router_backward(args[0], args[1], counts=got[1], coef=got[3], seq_offsets=args[3], mask=args[4])
+    bal = (got[1].cpu().numpy(), got[3].cpu().numpy(), 1.0, offsets, mask)
+    want = tuning.router_backward(logits, idx, balance=bal)
+    G = np.full((T, E), float((got[3][:, None] * got[1]).max()))
+    _check_grad(d, want, tuning.softmax_rows(logits), G)
+
+
+def test_logits_past_32_bit_offsets():
+    T, E, k, last = 2200000, 1024, 2, 100
+    logits = torch.zeros(T, E, dtype=torch.bfloat16, device=DEV)   # 2^31 elements before the last rows
+    logits[-last:].normal_(0, 2, generator=torch.Generator(DEV).manual_seed(1))
+    idx = torch.zeros(T, k, dtype=torch.int32, device=DEV)
+    idx[-last:] = torch.topk(logits[-last:].float(), k, dim=1).indices.int()
+    d_w = torch.zeros(T, k, device=DEV)
+    d_w[-last:].normal_(generator=torch.Generator(DEV).manual_seed(2))
+    offsets = torch.tensor([0, T - last, T], dtype=torch.int32, device=DEV)
+    loss, counts, prob, coef = gg.balance_loss(logits, idx, 0.5, offsets)
+    end = logits[-last:].contiguous(), idx[-last:].contiguous()
+    _, c1, p1, _ = gg.balance_loss(*end, 0.5)
+    assert torch.equal(counts[1:], c1) and int(counts[0, 0]) == (T - last) * k and not counts[0, 1:].any()
+    assert torch.allclose(prob[1:], p1, rtol=EPS, atol=0)
+    # equal logits: 1 / E each, summed over 2.2 million rows in chains of T / (2 * 148 * 8) and a tree behind them
+    assert torch.allclose(prob[0], torch.full((E,), 1 / E, device=DEV), rtol=T / (2 * 148 * 8) * 2 ** -24 + EPS, atol=0)
+    for renorm in (False, True):
+        d = gg.router_backward(logits, idx, d_w, renorm, out_dtype=torch.bfloat16)
+        assert torch.equal(d[-last:], gg.router_backward(*end, d_w[-last:].contiguous(), renorm, out_dtype=torch.bfloat16))
+        assert not d[:-last].any()

@@ -167,3 +167,55 @@ def test_combine_backward_of_slots_without_a_row(shared):
     assert np.all(np.abs(as_f64(dY) - wY) <= (2.0 ** -8 + 2.0 ** -23) * np.abs(wY))
     mag = tuning.combine_backward(dout.abs(), Y.nan_to_num().abs(), t2r, w, None)[1]
     assert np.all(np.abs(as_f64(dw) - ww) <= (d / 32 + 16) * 2.0 ** -24 * mag)
+
+
+def test_combine_backward_past_32_bit_offsets():
+    T, d, k = 40000, 7168, 8                                  # 2.3e9 elements of Y and of dY
+    rows = T * k
+    t2r = torch.arange(rows, dtype=torch.int32, device=DEV).view(T, k).flip(0).contiguous()
+    Y = torch.zeros(rows, d, dtype=torch.bfloat16, device=DEV)
+    Y[-k:], Y[:k] = 1, 2
+    dout = torch.zeros(T, d, dtype=torch.bfloat16, device=DEV)
+    dout[0], dout[-1] = 1, 3
+    w = torch.full((T, k), 0.5, device=DEV)
+    dY, dw = gg.combine_backward(dout, Y, t2r, w, False)
+    assert (dY[-k:] == 0.5).all() and (dY[:k] == 1.5).all() and not dY[k:-k].any()
+    assert (dw[0] == d).all() and (dw[-1] == 6 * d).all() and not dw[1:-1].any()
+
+
+def test_the_experts_input_gradient_with_adapters():
+    """dH of Y = H W2^T + s (H A^T) B^T by rows of experts: the frozen weights' part (a product in 32 bits here) goes in
+    as dx_base.  dY, dx_base and dH are rounded to bf16, half a step of 2^-8 each: 3 * 2^-8 of the norm at most."""
+    T, d, E, k, I, n, R = 80, 264, 4, 2, 136, 3, 24
+    g = torch.Generator().manual_seed(5)
+
+    def bf(*shape, std=1.0):
+        return (torch.randn(*shape, generator=g) * std).to(torch.bfloat16).to(DEV)
+
+    x, W2, A, B, gout = bf(T, d), bf(E, d, I, std=0.08), bf(n, R, I, std=0.1), bf(n, d, R, std=0.3), bf(T, d)
+    scale = torch.tensor([1.0, 0.5, 2.0], device=DEV)
+    idx = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).int().to(DEV)
+    w = torch.rand(T, k, generator=g).to(DEV)
+    plan = gg.permute(x, idx, E)
+    H, r2t = bf(T * k, I), plan["row_to_token"].long()
+    request = torch.randint(-1, n, (T,), generator=g, dtype=torch.int32).to(DEV)
+    row = request[r2t].contiguous()
+    off, order = gg.adapter_plan(row, n)
+    expert = torch.repeat_interleave(torch.arange(E, device=DEV), plan["counts"].long())
+
+    H64 = H.double().requires_grad_()
+    a = row.long().clamp(min=0)
+    low = torch.einsum("rni,ri->rn", A.double()[a], H64)
+    own = torch.einsum("rdn,rn->rd", B.double()[a], low) * (scale[a] * (row >= 0)).double()[:, None]
+    Y64 = torch.einsum("rdi,ri->rd", W2.double()[expert], H64) + own
+    slot = plan["token_to_row"].long()
+    out = (Y64[slot] * w.double()[:, :, None]).sum(1)
+    (out * gout.double()).sum().backward()
+
+    Y = Y64.detach().to(torch.bfloat16)
+    h = torch.where((row >= 0)[:, None], low, 0.0).detach().float()
+    dY, _ = gg.combine_backward(gout, Y, plan["token_to_row"], w, False)
+    frozen = torch.einsum("rdi,rd->ri", W2.float()[expert], dY.float()).to(torch.bfloat16)
+    dH, dA, dB = gg.lora_backward(dY, H, h, A, B, off, order, scale=scale, dx_base=frozen)
+    assert (dH.double() - H64.grad).norm() <= 3 * 2.0 ** -8 * H64.grad.norm()
+    assert torch.isfinite(dA).all() and torch.isfinite(dB).all()
