@@ -6,7 +6,9 @@ entry point of the same name on the current CUDA stream (the fine-tuning
 operators through _ops.so, which does the same in compiled code: their
 smallest calls take less time on the GPU than ctypes does on the host).  All computation
 happens in the library's CUDA kernels; there is no fallback path, and a
-missing or unloadable library raises immediately.
+missing or unloadable library raises immediately.  The calls stand outside
+autograd, the gradients' too: results are plain tensors whatever the inputs
+require, and a training step calls the gradients by name.
 
 Build the library with ``python -m grouped_gemm_03_b200.build``.
 """

@@ -19,10 +19,14 @@
 // One pass over the logits, each row held in registers by L lanes of 16 columns
 // (32 past 512 experts), the softmax's maximum and sum by shuffles, the next row
 // in flight.  The bytes alone would take 2.8 us (loss, 65536 tokens of 128
-// experts, fp16) and 5.5 (gradient, bf16); issue slots bound both: the loss's
-// first pass takes about 10 us and its second 8 (a chain of dependent loads and
-// the last block's sums), the gradient 17.  A batch of 128 tokens takes one
-// launch of 7 us, the gradient of 4096 tokens of 256 experts 6.
+// experts, fp16) and 5.5 (gradient, bf16); measured 18.5 and 14.5.  While an SM
+// is at work its issue slots are busy 52 % of the time in the loss's first pass
+// and 60 % in the gradient: a block has about 150 tokens, five rows to a lane
+// group, so what it does once (its sequence's search, the first loads, the
+// columns' sums through shared memory and their barriers) weighs as much as its
+// rows.  The loss's second launch is a chain of dependent loads and the last
+// block's sums.  A batch of 128 tokens takes one launch of 7 us, the gradient of
+// 4096 tokens of 256 experts 5.5.
 #include <type_traits>
 
 #include "common.cuh"

@@ -1,10 +1,10 @@
 // Argument marshalling of the fine-tuning operators, as the Python binding does
 // it for the layer's calls: types, shapes and devices are checked, outputs are
 // allocated with PyTorch, the C entry point is called on the current stream.
-// These calls are short (2 us of kernel on a decode batch), so the marshalling
-// is compiled: a call of combine_backward takes 4.5 us of host time here and 10.4
-// through ctypes and torch's Python functions; balance_loss, with its five
-// allocations, takes no more than its kernel's 9 against 17.
+// These calls are short (a kernel of under 5 us on a decode batch), so the
+// marshalling is compiled: a call of combine_backward takes 4.5 us of host time
+// here and 10.4 through ctypes and torch's Python functions; balance_loss, with
+// its five allocations, 7.1 against 17.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

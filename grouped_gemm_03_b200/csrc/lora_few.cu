@@ -12,10 +12,11 @@
 // terms; B's and A's next ranks are in flight while these are worked on.
 //
 // The least it has to do is to write dA and dB, 4 R (d + N) bytes an adapter;
-// beside that it is bound by issue slots (100 rows of 100 adapters, rank 64, 2048
-// and 2048 columns: 61 us, 105 MB of gradients).  The tensor-core passes start a
-// CTA and move 128 rows, most of them zeros, for each 256 columns of an adapter:
-// 145 us there.  few_rows() in lora_backward.cu has more of both.
+// beside that it is bound by latency (100 rows of 100 adapters, rank 64, 2048
+// and 2048 columns: 61 us, 105 MB of gradients; 11 warps to an SM keep its issue
+// slots 41 % busy and the shared memory's path 20 %).  The tensor-core passes
+// start a CTA and move 128 rows, most of them zeros, for each 256 columns of an
+// adapter: 133 us there.  few_rows() in lora_backward.cu has more of both.
 #include "common.cuh"
 #include "lora.cuh"
 #include "lora_tc.cuh"

@@ -26,7 +26,9 @@
  *     to a status word at the start of the caller's workspace; read it with
  *     moe_read_device_status after the work has run.
  *   - Inputs must be finite; NaN/Inf propagate unspecified.
- *   - Workspaces must be 256-byte aligned.
+ *   - Workspaces must be 256-byte aligned.  A size may depend on the number of
+ *     SMs: ask for it with the device current that the call will run on, and
+ *     for the sizes of that call (it does not always grow with them).
  */
 #ifndef MOE_B200_H
 #define MOE_B200_H
@@ -335,8 +337,10 @@ int moe_combine_backward(const void* dout, int dout_dtype, const void* Y, const 
  *   loss [1], prob [S, E] (or NULL), coef [S] fp32; counts [S, E] int32
  *   ws          moe_balance_loss_workspace_size(T, E, S) bytes (status + partial sums)
  * Status word: MOE_ERR_BAD_OFFSETS for bad seq_offsets, MOE_ERR_INVALID for an
- * id outside -1 .. E-1 (not counted).  Two launches; sums run in a fixed order.
- * E <= 1024, k <= min(E, 32), T * (k + 1) <= 2^30, S <= 2^20. */
+ * id outside -1 .. E-1 (not counted).  One launch up to 512 tokens, two past
+ * that; sums run in a fixed order, in fp32.  A probability whose numerator
+ * e^(logit - the row's largest) is below 2^-126 counts as 0.
+ * E <= 1024, k <= min(E, 32), T * (k + 1) <= 2^30, S <= 2^20; logits 16-byte aligned. */
 size_t moe_balance_loss_workspace_size(int T, int E, int S);
 int moe_balance_loss(const void* logits, int dtype, const int32_t* topk_idx, int T, int E, int k,
                      const int32_t* seq_offsets, int S, const uint8_t* token_mask, float alpha, float* loss,
@@ -358,8 +362,8 @@ int moe_balance_loss(const void* logits, int dtype, const int32_t* topk_idx, int
  *   d_loss      DEVICE fp32 scalar, the loss's own gradient, or NULL (1)
  *   d_logits    [T, E] d_dtype MOE_F32 | MOE_F16 | MOE_BF16.  A row that neither part
  *               reaches (no balance loss for the token, d_topk_w all 0) is 0 whatever its logits hold.
- * Limits as for moe_balance_loss.  d_logits may be logits itself when the
- * types are equal, and must not overlap it otherwise. */
+ * Limits as for moe_balance_loss; d_logits 16-byte aligned.  d_logits may be
+ * logits itself when the types are equal, and must not overlap it otherwise. */
 int moe_router_backward(const void* logits, int dtype, const int32_t* topk_idx, const float* d_topk_w, int T, int E,
                         int k, int renormalize, const int32_t* seq_offsets, int S, const uint8_t* token_mask,
                         const int32_t* counts, const float* coef, const float* d_loss, void* d_logits, int d_dtype,
@@ -396,8 +400,12 @@ int moe_adapter_plan(const int32_t* row_adapter, int rows, int n, int32_t* offse
  *          moe_lora_backward takes, or NULL
  *   ws     moe_lora_workspace_size(...) bytes (status + h); where that is 0, NULL, or a
  *          workspace of 256 bytes or more for the status word alone
- * fp32 sums, rounded once to out_dtype.  Status word (where there is a
- * workspace): MOE_ERR_TIMEOUT.  R a multiple of 8, 8 <= R <= 128
+ * fp32 sums, rounded once to out_dtype.  On the way h is held in bf16 terms, two
+ * for a bf16 result (2^-17 of h is left out) and three, all of an fp32 value, for
+ * an fp32 one; the tensor cores cut a sum off at 24 bits after every 16 products,
+ * where additions in fp32 would round it.  Status word (where there is a
+ * workspace): MOE_ERR_TIMEOUT.  n counts in the choice of launches as if all
+ * adapters had rows.  R a multiple of 8, 8 <= R <= 128
  * (pad smaller ranks with zeros); d % 8 == 0, N % 8 == 0, both <= 2^20; x, A, B,
  * base, out and h_out 16-byte aligned; out must not overlap x. */
 size_t moe_lora_workspace_size(int rows, int n, int d, int N, int R);
@@ -414,8 +422,9 @@ int moe_lora(const void* x, const void* A, const void* B, const float* scale, co
  *   dx      [rows, d] dx_dtype (MOE_BF16 | MOE_F32) or NULL (not wanted); may be dx_base itself
  *   dA [n, R, d], dB [n, N, R] grad_dtype (MOE_F32 | MOE_BF16), each or NULL; one of dx, dA, dB is given
  *   ws      moe_lora_backward_workspace_size(...) bytes (status + dh and partial sums)
- * Status word: MOE_ERR_TIMEOUT.  Sums run in a fixed order.  Shapes and alignment as for moe_lora; dx must
- * not overlap dC or x. */
+ * Status word: MOE_ERR_TIMEOUT.  Sums run in a fixed order, in fp32; dh and s h are held in bf16 terms as h in
+ * moe_lora (three for dA and dB, whatever their type), a tensor core's sum ends after 1024 rows of dA or dB and
+ * the rest is added in fp32.  Shapes and alignment as for moe_lora; dx must not overlap dC or x. */
 size_t moe_lora_backward_workspace_size(int rows, int n, int d, int N, int R);
 int moe_lora_backward(const void* dC, const void* x, const float* h, const void* A, const void* B, const float* scale,
                       const int32_t* offsets, const int32_t* order, int n, int rows, int d, int N, int R,
