@@ -114,6 +114,14 @@ def test_gradients_of_many_rows():
         assert _off(g, w) <= bound(steps)
 
 
+def test_gradients_of_many_rows_at_a_high_rank():
+    # above rank 64 the three terms take turns in one accumulator: three times the steps
+    s, (off, order) = _batch(3000, 2, 264, 128, 128, seed=4)
+    got = gg.lora_backward(s["dC"], s["x"], s["h"], s["A"], s["B"], off, order, scale=s["scale"], dx_dtype=torch.float32)
+    for g, w, steps in zip(got, _gradients(s, s["scale"]), (8 + 8, 8 + 3 * 64, 3 * 64)):
+        assert _off(g, w) <= bound(steps)
+
+
 @pytest.mark.parametrize("rows,n,R", [(12, 8, 64), (60, 100, 128), (40, 10, 16)])
 def test_gradients_of_few_rows(rows, n, R):
     # fp32 multiply-adds, rounded to nearest: N = 1032 columns in chains of up to 33, then sums over lanes, warps and CTAs
